@@ -41,6 +41,7 @@
 #ifndef FRT_H_
 #define FRT_H_
 
+#include <stddef.h>
 #include <stdint.h>
 #include <cuda_runtime_api.h>
 
@@ -407,6 +408,159 @@ frt_status frt_gate_residual_adarms_fp8(const void* x, const void* gate, const v
                                         uint8_t* out_fp8, const float* static_scale, float* block_scales,
                                         int M, int D, int rows_per_cond, float eps, frt_dtype dt, frt_quant qm,
                                         cudaStream_t stream);
+
+/*
+ * NVFP4 KV cache: a cache in 4 bits, its writer, its reader and the attention
+ * over it.
+ *
+ * Layout of one tensor (K or V) of a cache of `capacity` slots:
+ *   codes  uint8 [capacity, Hkv, hd/2]   e2m1 codes, two per byte, element 2j
+ *          in the low nibble of byte j; 16-byte aligned.
+ *   sf     uint8 [ceil(capacity/4), Hkv, hd/16, 4]   e4m3 scale factors of the
+ *          16-element blocks of a head: those of four neighbouring slots lie
+ *          side by side (slot s, block c of head g at byte
+ *          (((s / 4) Hkv + g) (hd/16) + c) 4 + s % 4); 16-byte aligned.
+ *          One 32-bit load brings a block's factors of four slots, which is
+ *          how a tensor-core tile of the attention wants them.
+ *   kv_scales  device fp32[2] = {k, v}: the per-tensor global scales gs, in
+ *          [2^-100, 2^100]; element ~ e2m1 * sf * gs.
+ * 4.5 bits an element: 0.28 of a 16-bit cache.
+ *
+ * frt_qkv_norm_rope_nvfp4_kvcache: op (b) with that cache.  Norm, RoPE and
+ * q_out as frt_qkv_norm_rope_kvcache; K after norm and RoPE, and V, are
+ * quantised in 16-element blocks:
+ *   y      = the exact K (or V) element rounded once to fp32 (K: norm and RoPE
+ *            carried in pairs of fp32 numbers, about 2^-45 relative),
+ *   sf     = e4m3(RN(amax_block * RN(1 / RN(6 gs))))   (RNE, saturating),
+ *   code   = e2m1(RN(y * RN(1 / RN(sf * gs))))         (RNE, saturating; 0
+ *            where sf is 0),
+ *   the decisions of the NVFP4 producers above.  A block that holds a NaN or
+ *   an infinity gets the NaN scale factor 0x7F and zero codes.
+ *   positions     device int32 [M], the RoPE positions.
+ *   slots         device int32 [M], the cache slots; NULL: slot = position.
+ *   status        as op (b), bit 0: a row whose position is outside
+ *                 [0, max_pos) or whose slot is outside [0, capacity) is
+ *                 skipped entirely (a slot of -1 marks a padding row).
+ *   Two rows of one call with the same slot leave it unspecified.
+ *   16-bit pointers, cos_tab and sin_tab 16-byte aligned.
+ *   Layout rule: Hq, Hkv > 0, Hq % Hkv == 0, hd > 0 and hd % 16 == 0,
+ *   max_pos > 0, capacity > 0.  Unsupported: hd > 256.
+ *
+ * frt_nvfp4_kvcache_read: rows of the cache back in 16 bits:
+ *   k_out[i, g, :] = code * sf * gs of slot slots[i] (code * sf exact, one
+ *   rounding to fp32 for the product with gs, one to 16 bits); v_out likewise.
+ *   slots         device int32 [n]; NULL: slot i.
+ *   k_out, v_out  device [n, Hkv, hd] 16-bit, 16-byte aligned.
+ *   status        bit 0: a slot outside [0, capacity); its rows stay as they
+ *                 were.
+ *   Layout rule: n >= 0, Hkv, capacity > 0, hd > 0 and hd % 16 == 0.
+ *   Unsupported: hd > 256.
+ */
+frt_status frt_qkv_norm_rope_nvfp4_kvcache(const void* qkv, const void* q_norm_w, const void* k_norm_w,
+                                           const float* cos_tab, const float* sin_tab, const int32_t* positions,
+                                           const int32_t* slots, void* q_out, uint8_t* k_codes, uint8_t* k_sf,
+                                           uint8_t* v_codes, uint8_t* v_sf, const float* kv_scales, int32_t* status,
+                                           int M, int Hq, int Hkv, int hd, int max_pos, int capacity, float eps,
+                                           frt_dtype dt, cudaStream_t stream);
+frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8_t* k_sf, const uint8_t* v_codes,
+                                  const uint8_t* v_sf, const float* kv_scales, const int32_t* slots, void* k_out,
+                                  void* v_out, int32_t* status, int n, int Hkv, int hd, int capacity, frt_dtype dt,
+                                  cudaStream_t stream);
+
+/*
+ * frt_attn_nvfp4_kvcache: softmax attention over an NVFP4 KV cache.
+ *
+ *   out[i, h, :] = sum_p w[p] v[p] / sum_p w[p],   w[p] = exp(softmax_scale *
+ *                  q[i, h, :] . k[p] - max),
+ *   p over the positions [max(0, kv_len[i] - window), kv_len[i]) of token i's
+ *   sequence (window <= 0: from position 0), k and v those of KV head
+ *   h / (Hq / Hkv).  A token that sees no position gets zeros.
+ *   kv_len[i] = position + 1 makes the attention causal, the same kv_len for
+ *   all tokens of a sequence makes it bidirectional, an encoder's length makes
+ *   it cross attention.
+ *   Scores, softmax statistics and output sums are fp32; the weights w are
+ *   rounded to fp16 (scaled so that weights down to 2^-25 of the row's largest
+ *   keep 11 bits) and their sum is the sum of the rounded ones; the output is
+ *   rounded once to 16 bits.  No atomics: the same call gives the same bits.
+ *
+ *   q, out        device [M, Hq, hd] 16-bit, 16-byte aligned.
+ *   codes, sf, kv_scales   the cache, as above.
+ *   kv_len        device int32 [M].
+ *   q_indptr      device int32 [n_seqs + 1]: sequence b holds tokens
+ *                 q_indptr[b] .. q_indptr[b+1] - 1 (ascending, within [0, M]);
+ *                 NULL (n_seqs == 1 only): all M tokens.  Tokens of no sequence
+ *                 are left as they were in out.
+ *   page_table    device int32 [n_seqs, max_pages]: position p of sequence b
+ *                 is slot page_table[b, p / page_size] * page_size + p %
+ *                 page_size.  page_size % 4 == 0.  NULL: slot = position for
+ *                 every sequence (page_size and max_pages ignored).  Entries
+ *                 past a sequence's last page are not read.
+ *   max_q_len     host bound on the tokens of a sequence.
+ *   max_kv_len    host bound on kv_len.  Both size the launch only: the work
+ *                 follows the device lengths.
+ *   workspace     device, 16-byte aligned, at least
+ *                 frt_attn_nvfp4_workspace_bytes(...) bytes (the caller's;
+ *                 contents need no preparation and mean nothing afterwards).
+ *                 Calls that may run at the same time need one each.  NULL if
+ *                 that size is 0.
+ *   status        device int32[1] or NULL; bits set with an atomic OR, never
+ *                 cleared:  bit 0  a kv_len below 0 or above max_kv_len, or one
+ *                 that reaches past the capacity or the page table (clamped);
+ *                 or a q_indptr that is out of order, outside [0, M] or gives a
+ *                 sequence more than max_q_len tokens (the extra tokens are
+ *                 left as they were); or a page outside [0, capacity /
+ *                 page_size) (its positions are left out).
+ *   NaN: a NaN scale factor in a position that a row sees makes that row NaN;
+ *   whatever unseen positions hold has no effect.
+ *   Layout rule: Hq, Hkv > 0, Hq % Hkv == 0, hd > 0 and hd % 16 == 0,
+ *   n_seqs > 0, capacity > 0, max_q_len > 0, max_kv_len >= 0, softmax_scale
+ *   finite; n_seqs == 1 without q_indptr.  Unsupported: hd > 256, more than
+ *   65535 sequences, max_kv_len > 2^31 - 256.
+ */
+size_t frt_attn_nvfp4_workspace_bytes(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len);
+frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_codes, const uint8_t* k_sf, const uint8_t* v_codes,
+                                  const uint8_t* v_sf, const float* kv_scales, const int32_t* kv_len,
+                                  const int32_t* q_indptr, const int32_t* page_table, void* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* status, int M, int n_seqs, int Hq, int Hkv, int hd,
+                                  int capacity, int page_size, int max_pages, int max_q_len, int max_kv_len,
+                                  int window, float softmax_scale, frt_dtype dt, cudaStream_t stream);
+
+/* Rows of the matrix-vector product below:
+ *   16BIT        the op's 16-bit type
+ *   E4M3         FP8 codes, one static scale (frt_residual_rmsnorm_fp8 and
+ *                frt_gate_act_fp8 with FRT_QUANT_STATIC)
+ *   E4M3_BLOCK   FP8 codes, per-row block-128 scales (FRT_QUANT_BLOCK128)
+ *   NVFP4        the NVFP4 producers' output */
+typedef enum { FRT_X_16BIT = 0, FRT_X_E4M3 = 1, FRT_X_E4M3_BLOCK = 2, FRT_X_NVFP4 = 3 } frt_x_format;
+
+/*
+ * Matrix-vector products with NVFP4 weights, for the few rows of a decoding or
+ * action step (any M is accepted; the kernel is built for M up to about 64):
+ *   y[i, n] = sum_k x[i, k] w[n, k] + bias[n],
+ *   w[n, k] = e2m1 code * sf[n, k / 16] * w_scale,
+ * x as the 16-bit type or as this library's FP8 / NVFP4 ops wrote it.  Products
+ * are exact, sums fp32, one rounding to 16 bits.  (bf16 rows are carried as
+ * fp16 times a power of two per row and 128 columns: exact down to 2^-28 of the
+ * block's largest magnitude, and below that to 2^-39 of it.)
+ *
+ *   x         device [M, K] 16-bit or e4m3 bytes, or [M, K/2] e2m1 bytes.
+ *   x_scales  device fp32: 16BIT ignored; E4M3 [1]; E4M3_BLOCK [M,
+ *             ceil(K/128)]; NVFP4 [1], the global scale.
+ *   x_sf      NVFP4: device bytes in `sf_layout`, [M, K/16]; else ignored.
+ *   w_codes   device [N, K/2] bytes.
+ *   w_sf      device bytes in `sf_layout`, [N, K/16].
+ *   w_scale   device fp32[1].
+ *   bias      device [N] 16-bit, or NULL.
+ *   y         device [M, N] 16-bit.
+ *   w_codes, w_sf, w_scale and bias are constant inputs (see frt_set_pdl): the
+ *   kernel launched just before on the same stream must not write them.
+ *   x, w_codes, x_sf and w_sf 16-byte aligned; bias and y 2-byte, x_scales and
+ *   w_scale 4-byte.
+ *   Layout rule: N > 0, K > 0 and K % 16 == 0.  M == 0 does nothing.
+ */
+frt_status frt_matvec_nvfp4(const void* x, const float* x_scales, const uint8_t* x_sf, const uint8_t* w_codes,
+                            const uint8_t* w_sf, const float* w_scale, const void* bias, void* y, int M, int N, int K,
+                            frt_x_format x_format, frt_sf_layout sf_layout, frt_dtype dt, cudaStream_t stream);
 
 /*
  * Empty kernel used to measure the launch floor that the ops above are graded

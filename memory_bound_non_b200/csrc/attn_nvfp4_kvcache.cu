@@ -1,0 +1,832 @@
+// Softmax attention over an NVFP4 KV cache: one pass over the keys with a
+// running maximum and sum, the keys split over warps and CTAs.
+//
+// What bounds it: a decoding step reads each cached code and factor once
+// (1.125 hd bytes a slot and KV head) and does 4 hd operations per query head
+// on it, so few query rows are bound by HBM; the codes' conversion (one cvt and
+// one multiply per two elements) has to stay below that, many rows are bound by
+// the tensor cores.
+//
+// Mapping.  A warp takes tiles of 32 slots of one KV head and computes with
+// the keys on the 16-row side of mma.m16n8k16, 8 NT query rows on the other:
+//   S^T = K Q^T,  O^T = V^T P^T.
+// The order of dimensions inside a product is free, so each lane (g = lane / 4,
+// t = lane % 4) loads long runs: of K the slots 4g .. 4g+3 at dimensions
+// 16 J t .. 16 J (t+1) - 1 (J = HD / 64), of V the slots 8t .. 8t+7 at
+// dimensions 8 J g .. 8 J (g+1) - 1.  One 32-bit word of the cache's factors
+// holds a block's factors of four neighbouring slots: those of a lane's K rows,
+// and with a second word the pairs (8t + i, 8t + 4 + i) that V needs.  V's
+// operand wants two slots in one register: lo = (a & 0x0F..) | (b << 4 &
+// 0xF0..) and the same for the high nibbles puts two slots' codes of one
+// dimension into a byte before the conversion, half an instruction a
+// conversion.  The weights go from S^T's layout (slot by row) to P^T's (slot by
+// pairs of rows) with one 8x8 transpose for 8 slots.
+//
+// Weights: p = 2^(s - m + 11) in fp32, rounded to binary16; m is the row's
+// maximum when it was last renewed, which happens when a score passes m by more
+// than 4, so 2^11 <= p <= 2^15 for the largest and weights down to 2^-25 of it
+// are normal numbers.  The sum is taken of the rounded weights (a row of ones
+// beside V).  bf16 queries enter as binary16 times a power of two per row.
+#include <cmath>
+
+#include "frt_device.cuh"
+#include "frt_host.h"
+
+namespace frt {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 32;  // slots
+constexpr int kSMs = 148;
+
+struct Args {
+  const void* q;
+  const uint8_t* k_codes;
+  const uint8_t* k_sf;
+  const uint8_t* v_codes;
+  const uint8_t* v_sf;
+  const float* kv_scales;
+  const int32_t* kv_len;
+  const int32_t* q_indptr;
+  const int32_t* page_table;
+  void* out;
+  float2* part_ml;  // [chunk][M Hq] (maximum, sum)
+  float* part_o;    // [chunk][M Hq][hd]
+  int32_t* status;
+  int M, n_seqs, Hq, Hkv, hd, group;
+  int capacity, page_size, max_pages, n_pages;
+  int max_q_len, max_len;  // max_len: the largest length a token may have
+  int window;
+  uint32_t page_mul;  // p / page_size = (p + umulhi(p, page_mul)) >> page_shift
+  int page_shift;
+  int row_tiles, chunks, chunk_tiles;
+  float scale_log2;
+  int dt;
+};
+
+// Tokens [t0, t0 + n) of a sequence.
+struct Seq {
+  int t0, n;
+  bool bad;
+};
+__device__ __forceinline__ Seq sequence(const Args& a, int b) {
+  int s0 = 0, s1 = a.M;
+  if (a.q_indptr != nullptr && FRT_SPAN_OK(b, 2, a.n_seqs + 1)) {
+    s0 = __ldg(a.q_indptr + b);
+    s1 = __ldg(a.q_indptr + b + 1);
+  }
+  Seq s;
+  s.bad = s0 < 0 || s1 > a.M || s1 < s0;
+  s0 = min(max(s0, 0), a.M);
+  s1 = min(max(s1, s0), a.M);
+  s.t0 = s0;
+  s.n = s1 - s0;
+  if (s.n > a.max_q_len) {
+    s.n = a.max_q_len;
+    s.bad = true;
+  }
+  return s;
+}
+
+// The R query rows of a CTA (token-major, then the heads of the group) and the
+// positions they see.  Computed by every warp for itself, one row a lane (two
+// for R = 64).
+struct Rows {
+  int lo, hi;            // this lane's row: positions [lo, hi); empty: lo >= hi
+  int tok;               // its token, or -1
+  int head;              // its query head
+  int all_lo, all_hi;    // the positions that any row sees (empty: all_hi <= all_lo)
+  int full_lo, full_hi;  // the positions that every row sees
+  int tiles;             // kTile-slot tiles from first() on
+  bool bad;
+  __device__ __forceinline__ int first() const { return all_lo & ~3; }
+};
+template <int R>
+__device__ __forceinline__ Rows query_rows(const Args& a, int b, int rt, int kvh) {
+  static_assert(R <= 32, "one row a lane");
+  const Seq s = sequence(a, b);
+  const int lane = threadIdx.x & 31;
+  const int r = rt * R + lane;
+  Rows o;
+  o.bad = s.bad;
+  o.tok = -1;
+  o.head = 0;
+  o.lo = o.hi = 0;
+  if (lane < R && r / a.group < s.n) {
+    const int tok = s.t0 + r / a.group;
+    o.tok = tok;
+    o.head = kvh * a.group + r % a.group;
+    if (FRT_IDX_OK(tok, a.M)) {
+      const int len = __ldg(a.kv_len + tok);
+      o.hi = min(max(len, 0), a.max_len);
+      o.bad |= o.hi != len;
+      o.lo = a.window > 0 ? max(0, o.hi - a.window) : 0;
+    }
+  }
+  const bool sees = o.hi > o.lo;
+  o.all_lo = __reduce_min_sync(0xFFFFFFFFu, sees ? o.lo : 0x7FFFFFFF);
+  o.all_hi = __reduce_max_sync(0xFFFFFFFFu, sees ? o.hi : 0);
+  o.full_lo = __reduce_max_sync(0xFFFFFFFFu, o.tok >= 0 ? o.lo : 0);
+  o.full_hi = __reduce_min_sync(0xFFFFFFFFu, o.tok >= 0 ? o.hi : 0x7FFFFFFF);
+  if (o.all_hi <= o.all_lo) o.all_lo = o.all_hi = 0;
+  const int span = o.all_hi - o.first();
+  o.tiles = span / kTile + (span % kTile != 0);
+  return o;
+}
+
+__device__ __forceinline__ uint32_t select_bits(uint32_t mask, uint32_t a, uint32_t b) {
+  return (a & mask) | (b & ~mask);
+}
+
+// HD: head dimension of the build (a multiple of 64, at least hd); EXACT: hd ==
+// HD; NT: query rows / 8.
+template <int HD, bool EXACT, int NT>
+struct Attn {
+  static constexpr int J = HD / 64;
+  static constexpr int R = 8 * NT;
+  static constexpr int kSteps = HD / 16;
+  static constexpr int kVs = J == 3 ? 3 : (J + 1) / 2;  // factor words a lane and quad of V
+  static constexpr int kOStride = HD + 4;
+  static constexpr size_t kQBytes = (size_t)kSteps * NT * 32 * 8;
+  static constexpr size_t kMergeBytes = (size_t)kWarps * R * kOStride * 4;
+  static constexpr size_t kSmem = (kQBytes > kMergeBytes ? kQBytes : kMergeBytes) + R * 4 + 2 * kWarps * R * 4;
+
+  struct KFrag {
+    uint32_t c[4][2 * J];
+    uint32_t sf[J];
+  };
+  struct VFrag {
+    uint32_t c[2][4][J];
+    uint32_t sf[2][kVs];
+  };
+
+  // First slot of the quad of positions pos .. pos + 3, or -1 (behind the end,
+  // or on a page that does not exist).
+  static __device__ __forceinline__ int quad_slot(const Args& a, int b, int pos, const Rows& rows) {
+    if (pos >= rows.all_hi) return -1;
+    if (a.page_table == nullptr) return pos;
+    const int page = (int)((__umulhi((uint32_t)pos, a.page_mul) + (uint32_t)pos) >> a.page_shift);
+    const int64_t at = (int64_t)b * a.max_pages + page;
+    if (!FRT_IDX_OK(at, (int64_t)a.n_seqs * a.max_pages)) return -1;
+    const int entry = __ldg(a.page_table + at);
+    if (entry < 0 || entry >= a.n_pages) {
+      if (a.status != nullptr && pos + 3 >= rows.all_lo) atomicOr(a.status, 1);
+      return -1;
+    }
+    return entry * a.page_size + (pos - page * a.page_size);
+  }
+
+  static __device__ __forceinline__ void load_k(const Args& a, int kvh, int slot, int count, int t, KFrag& f) {
+    const int nblk = a.hd >> 4;
+    const int64_t row_bytes = (int64_t)a.Hkv * (a.hd >> 1);
+    const int64_t code0 = (int64_t)slot * row_bytes + (int64_t)kvh * (a.hd >> 1) + t * 8 * J;
+    const uint8_t* p = a.k_codes + code0;
+    const int64_t code_bytes = row_bytes * a.capacity;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool on = slot >= 0 && i < count;
+      const uint8_t* pi = p + i * row_bytes;
+      if (EXACT && (J & 1) == 0) {
+#pragma unroll
+        for (int j = 0; j < J; j += 2) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (on && FRT_SPAN_OK(code0 + i * row_bytes + 8 * j, 16, code_bytes))
+            v = ld_stream(reinterpret_cast<const uint4*>(pi + 8 * j));
+          f.c[i][2 * j] = v.x;
+          f.c[i][2 * j + 1] = v.y;
+          f.c[i][2 * j + 2] = v.z;
+          f.c[i][2 * j + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          uint2 v = make_uint2(0, 0);
+          if (on && (EXACT || t * J + j < nblk) && FRT_SPAN_OK(code0 + i * row_bytes + 8 * j, 8, code_bytes))
+            v = ld_stream(reinterpret_cast<const uint2*>(pi + 8 * j));
+          f.c[i][2 * j] = v.x;
+          f.c[i][2 * j + 1] = v.y;
+        }
+      }
+    }
+    const int64_t word0 = ((int64_t)(slot >> 2) * a.Hkv + kvh) * nblk + t * J;
+    const int64_t words = (int64_t)((a.capacity + 3) >> 2) * a.Hkv * nblk;
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(a.k_sf);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      f.sf[j] = 0;
+      if (slot >= 0 && (EXACT || t * J + j < nblk) && FRT_IDX_OK(word0 + j, words)) f.sf[j] = __ldg(s + word0 + j);
+    }
+  }
+
+  // Slots of quad 0 (slot0) and 1 (slot1), `count` valid slots in each.
+  static __device__ __forceinline__ void load_v(const Args& a, int kvh, int slot0, int slot1, int count0, int count1,
+                                                int g, VFrag& f) {
+    const int nblk = a.hd >> 4;
+    const int64_t row_bytes = (int64_t)a.Hkv * (a.hd >> 1);
+    const int64_t code_bytes = row_bytes * a.capacity;
+    const int64_t words = (int64_t)((a.capacity + 3) >> 2) * a.Hkv * nblk;
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(a.v_sf);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int slot = h == 0 ? slot0 : slot1;
+      const int count = h == 0 ? count0 : count1;
+      const int64_t code0 = (int64_t)slot * row_bytes + (int64_t)kvh * (a.hd >> 1) + g * 4 * J;
+      const uint8_t* p = a.v_codes + code0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool on = slot >= 0 && i < count;
+        const uint8_t* pi = p + i * row_bytes;
+        const int64_t at = code0 + i * row_bytes;
+        if (J == 4 && EXACT) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (on && FRT_SPAN_OK(at, 16, code_bytes)) v = ld_stream(reinterpret_cast<const uint4*>(pi));
+          f.c[h][i][0] = v.x;
+          f.c[h][i][1 % J] = v.y;
+          f.c[h][i][2 % J] = v.z;
+          f.c[h][i][3 % J] = v.w;
+        } else if ((J & 1) == 0) {
+#pragma unroll
+          for (int j = 0; j < J; j += 2) {
+            uint2 v = make_uint2(0, 0);
+            if (on && (EXACT || g * J + j < 2 * nblk) && FRT_SPAN_OK(at + 4 * j, 8, code_bytes))
+              v = ld_stream(reinterpret_cast<const uint2*>(pi + 4 * j));
+            f.c[h][i][j] = v.x;
+            f.c[h][i][(j + 1) % J] = v.y;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            f.c[h][i][j] = 0;
+            if (on && (EXACT || g * J + j < 2 * nblk) && FRT_SPAN_OK(at + 4 * j, 4, code_bytes))
+              f.c[h][i][j] = __ldg(reinterpret_cast<const uint32_t*>(pi + 4 * j));
+          }
+        }
+      }
+      // factors of slots behind the end may hold anything: cleared
+      const uint32_t keep = count >= 4 ? 0xFFFFFFFFu : (1u << (8 * max(count, 0))) - 1;
+      const int64_t word0 = ((int64_t)(slot >> 2) * a.Hkv + kvh) * nblk;
+#pragma unroll
+      for (int j = 0; j < kVs; ++j) {
+        const int blk = (g * J + (J == 3 ? j : 2 * j)) >> 1;
+        f.sf[h][j] = 0;
+        if (slot >= 0 && (EXACT || blk < nblk) && FRT_IDX_OK(word0 + blk, words))
+          f.sf[h][j] = __ldg(s + word0 + blk) & keep;
+      }
+    }
+  }
+
+  // Bytes that hold the NaN factor, marked in their top bits.
+  static __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  }
+};
+
+template <int HD, bool EXACT, int NT>
+__host__ __device__ constexpr int min_ctas() {
+  return HD / 64 * NT <= 2 ? 4 : HD / 64 * NT <= 4 && HD <= 128 ? 3 : 2;
+}
+
+template <int HD, bool EXACT, int NT>
+__global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kernel(const Args a) {
+  using A = Attn<HD, EXACT, NT>;
+  constexpr int J = A::J, R = A::R;
+  extern __shared__ __align__(16) unsigned char smem[];
+  uint2* q_frag = reinterpret_cast<uint2*>(smem);
+  float* merge_o = reinterpret_cast<float*>(smem);
+  float* q_scale = reinterpret_cast<float*>(smem + A::kSmem - R * 4 - 2 * kWarps * R * 4);
+  float* merge_m = q_scale + R;
+  float* merge_l = merge_m + kWarps * R;
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int b = blockIdx.y;
+  // heads are neighbours in the grid: CTAs that run at the same time read
+  // neighbouring bytes of a slot
+  int x = blockIdx.x;
+  const int kvh = x % a.Hkv;
+  x /= a.Hkv;
+  const int rt = x % a.row_tiles;
+  const int chunk = x / a.row_tiles;
+
+  pdl_enter();
+  const Rows rows = query_rows<R>(a, b, rt, kvh);
+  if (rows.bad && a.status != nullptr) atomicOr(a.status, 1);
+  const int tile0 = chunk * a.chunk_tiles;
+  if (rows.full_hi == 0x7FFFFFFF || (chunk > 0 && tile0 >= rows.tiles)) return;  // no rows, or no work
+  const int tile1 = min(tile0 + a.chunk_tiles, rows.tiles);
+
+  const float gs_k = __ldg(a.kv_scales), gs_v = __ldg(a.kv_scales + 1);
+
+  // first loads, on their way while the queries are laid out
+  typename A::KFrag kf;
+  typename A::VFrag vf;
+  int tile = tile0 + warp;
+  auto position = [&](int tl) { return rows.first() + tl * kTile + 4 * g; };
+  auto slot_of = [&](int tl) { return tl < tile1 ? A::quad_slot(a, b, position(tl), rows) : -1; };
+  auto fetch_k = [&](int tl, int slot) { A::load_k(a, kvh, slot, rows.all_hi - position(tl), t, kf); };
+  auto fetch_v = [&](int tl, int slot) {
+    const int s0 = __shfl_sync(0xFFFFFFFFu, slot, 8 * t), s1 = __shfl_sync(0xFFFFFFFFu, slot, 8 * t + 4);
+    const int left = rows.all_hi - (rows.first() + tl * kTile + 8 * t);
+    A::load_v(a, kvh, s0, s1, left, left - 4, g, vf);
+  };
+  int slot = slot_of(tile);
+  int slot_next = slot_of(tile + kWarps);
+  fetch_k(tile, slot);
+  fetch_v(tile, slot);
+
+  // queries: a warp a row, in the order that the lanes read them
+  for (int r = warp; r < R; r += kWarps) {
+    const int tok = __shfl_sync(0xFFFFFFFFu, rows.tok, r), head = __shfl_sync(0xFFFFFFFFu, rows.head, r);
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (tok >= 0 && lane < a.hd / 8) {
+      const int64_t at = ((int64_t)tok * a.Hq + head) * (a.hd / 8) + lane;
+      if (FRT_IDX_OK(at, (int64_t)a.M * a.Hq * (a.hd / 8))) raw = ld_plain(static_cast<const uint4*>(a.q) + at);
+    }
+    float s = 1.0f;
+    if (a.dt == FRT_BF16) {
+      float2 v[4];
+      unpack_pairs<FRT_BF16, 4>(&raw.x, v);
+      float amax = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
+      s = pow2_to_half_range(warp_max_abs(amax));
+      mul_pairs<4>(v, s);
+      pack_pairs<FRT_F16, 4>(v, &raw.x);
+    }
+    if (lane < HD / 8) {
+      const int blk = lane >> 1;
+      const int step = (blk % J) * 4 + (lane & 1) * 2;
+      uint2* dst = q_frag + ((step * NT + (r >> 3)) * 32 + (r & 7) * 4 + blk / J);
+      dst[0] = make_uint2(raw.x, raw.y);
+      dst[NT * 32] = make_uint2(raw.z, raw.w);
+    }
+    if (lane == 0) q_scale[r] = a.scale_log2 * gs_k / s;
+  }
+  __syncthreads();
+
+  const float kInf = __int_as_float(0x7F800000);
+  float c[NT][2], m[NT][2];
+  int lo[NT][2], hi[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * n + 2 * t + e;
+      c[n][e] = q_scale[r];
+      m[n][e] = -kInf;
+      lo[n][e] = __shfl_sync(0xFFFFFFFFu, rows.lo, r);
+      hi[n][e] = __shfl_sync(0xFFFFFFFFu, rows.hi, r);
+    }
+  float o[NT][HD / 16][4], l[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int i = 0; i < HD / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
+    l[n][0] = l[n][1] = l[n][2] = l[n][3] = 0.0f;
+  }
+
+  for (; tile < tile1; tile += kWarps) {
+    const int slot_after = slot_of(tile + 2 * kWarps);
+    const int pos = position(tile);
+    const int pos0 = pos - 4 * g;
+    // ---- S^T = K Q^T
+    float s[NT][8];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[n][e] = 0.0f;
+#pragma unroll
+    for (int jb = 0; jb < J; ++jb) {
+      uint32_t sc[4];
+      e4m3x4_to_half2(__byte_perm(kf.sf[jb], 0, 0x1100), sc);
+      e4m3x4_to_half2(__byte_perm(kf.sf[jb], 0, 0x3322), sc + 2);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t h[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e2m1x8_to_half2(kf.c[i][2 * jb + w], h[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[i][e] = hmul2(h[i][e], sc[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t a0[4] = {h[0][2 * j], h[1][2 * j], h[0][2 * j + 1], h[1][2 * j + 1]};
+          const uint32_t a1[4] = {h[2][2 * j], h[3][2 * j], h[2][2 * j + 1], h[3][2 * j + 1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint2 qb = q_frag[((jb * 4 + w * 2 + j) * NT + n) * 32 + lane];
+            mma_16816(s[n], a0, qb.x, qb.y);
+            mma_16816(s[n] + 4, a1, qb.x, qb.y);
+          }
+        }
+      }
+    }
+    fetch_k(tile + kWarps, slot_next);
+
+    // ---- masks.  A NaN factor of V turns the weights of its slot NaN (for
+    // the rows that see it) and counts as zero itself, so that it cannot reach
+    // other rows.
+    uint32_t bad = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < A::kVs; ++j) bad |= A::nan_bytes(vf.sf[h][j]);
+    if (__any_sync(0xFFFFFFFFu, bad != 0)) {
+      uint32_t nan_slots = 0;  // bit 8t + 4h + i
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t mark = 0;
+#pragma unroll
+        for (int j = 0; j < A::kVs; ++j) {
+          const uint32_t nb = A::nan_bytes(vf.sf[h][j]);
+          mark |= nb;
+          vf.sf[h][j] &= ~((nb >> 7) * 0xFFu);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((mark >> (8 * i + 7)) & 1) nan_slots |= 1u << (8 * t + 4 * h + i);
+      }
+      nan_slots = __reduce_or_sync(0xFFFFFFFFu, nan_slots);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((nan_slots >> (4 * g + i)) & 1) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            s[n][2 * i] = s[n][2 * i + 1] = __int_as_float(0x7FC00000);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[n][e] *= c[n][e & 1];
+    if (pos0 < rows.full_lo || pos0 + kTile > rows.full_hi || __any_sync(0xFFFFFFFFu, slot < 0)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (slot < 0 || pos + i < lo[n][e] || pos + i >= hi[n][e]) s[n][2 * i + e] = -kInf;
+    }
+
+    // ---- running maximum, renewed when a score passes it by more than 4
+    bool above = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float top = fmaxf(fmaxf(s[n][e], s[n][2 + e]), fmaxf(s[n][4 + e], s[n][6 + e]));
+        above |= top > m[n][e] + 4.0f;
+      }
+    if (__any_sync(0xFFFFFFFFu, above)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(fmaxf(s[n][e], s[n][2 + e]), fmaxf(s[n][4 + e], s[n][6 + e]));
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          if (top > m[n][e]) {
+            const float f = ex2_approx(m[n][e] - top);
+            m[n][e] = top;
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+              o[n][i][e] *= f;
+              o[n][i][2 + e] *= f;
+            }
+            l[n][e] *= f;
+            l[n][2 + e] *= f;
+          }
+        }
+    }
+
+    // ---- weights, and their move to P^T's layout
+    uint32_t p[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float shift[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) shift[e] = (m[n][e] == -kInf ? 0.0f : m[n][e]) - 11.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        p[n][i] = transpose_8x8(Pack16<FRT_F16>::from_float2(ex2_approx(s[n][2 * i] - shift[0]),
+                                                             ex2_approx(s[n][2 * i + 1] - shift[1])));
+      const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+      mma_16816(l[n], ones, p[n][0], p[n][1]);
+      mma_16816(l[n], ones, p[n][2], p[n][3]);
+    }
+
+    // ---- O^T += V^T P^T
+    uint32_t sc[4];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int js = J == 3 ? j : j / 2;
+      if (J == 3 || (j & 1) == 0) {
+        e4m3x4_to_half2(__byte_perm(vf.sf[0][js], vf.sf[1][js], 0x5140), sc);
+        e4m3x4_to_half2(__byte_perm(vf.sf[0][js], vf.sf[1][js], 0x7362), sc + 2);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // slot pairs 2k, 2k + 1
+        uint32_t low[2][4], high[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t va = vf.c[0][2 * k + i][j], vb = vf.c[1][2 * k + i][j];
+          e2m1x8_to_half2(select_bits(0x0F0F0F0Fu, va, vb << 4), low[i]);
+          e2m1x8_to_half2(select_bits(0x0F0F0F0Fu, va >> 4, vb), high[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            low[i][e] = hmul2(low[i][e], sc[2 * k + i]);
+            high[i][e] = hmul2(high[i][e], sc[2 * k + i]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t av[4] = {low[0][e], high[0][e], low[1][e], high[1][e]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_16816(o[n][4 * j + e], av, p[n][2 * k], p[n][2 * k + 1]);
+        }
+      }
+    }
+    fetch_v(tile + kWarps, slot_next);
+    slot = slot_next;
+    slot_next = slot_after;
+  }
+
+  // ---- the warps' parts joined
+  if (g == 0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) merge_m[warp * R + 8 * n + 2 * t + e] = m[n][e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * n + 2 * t + e;
+      float top = merge_m[r];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_m[w * R + r]);
+      const float f = m[n][e] == -kInf ? 0.0f : ex2_approx(m[n][e] - top);
+      float* row = merge_o + (size_t)(warp * R + r) * A::kOStride + g * 8 * J;
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i)
+        *reinterpret_cast<float2*>(row + 2 * i) = make_float2(o[n][i][e] * f, o[n][i][2 + e] * f);
+      if (g == 0) merge_l[warp * R + r] = l[n][e] * f;
+    }
+  __syncthreads();
+  const bool whole = rows.tiles <= a.chunk_tiles;  // this CTA saw all of the keys
+  const int quarter = a.hd / 4;
+  for (int i = threadIdx.x; i < R * quarter; i += kThreads) {
+    const int r = i / quarter, d = (i - r * quarter) * 4;
+    // row r's token and head, as query_rows gives them
+    const int rr = rt * R + r;
+    const Seq sq = sequence(a, b);
+    if (rr / a.group >= sq.n) continue;
+    const int64_t row = (int64_t)(sq.t0 + rr / a.group) * a.Hq + kvh * a.group + rr % a.group;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 u = *reinterpret_cast<const float4*>(merge_o + (size_t)(w * R + r) * A::kOStride + d);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+      sum += merge_l[w * R + r];
+    }
+    const int64_t at = row * a.hd + d;
+    if (whole) {
+      const float f = sum == 0.0f ? 0.0f : gs_v / sum;
+      const uint2 w = a.dt == FRT_F16 ? make_uint2(Pack16<FRT_F16>::from_float2(v.x * f, v.y * f),
+                                                   Pack16<FRT_F16>::from_float2(v.z * f, v.w * f))
+                                      : make_uint2(Pack16<FRT_BF16>::from_float2(v.x * f, v.y * f),
+                                                   Pack16<FRT_BF16>::from_float2(v.z * f, v.w * f));
+      if (FRT_SPAN_OK(at, 4, (int64_t)a.M * a.Hq * a.hd))
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = w;
+    } else {
+      const int64_t n_rows = (int64_t)a.M * a.Hq;
+      const int64_t part = (int64_t)chunk * n_rows;
+      if (FRT_SPAN_OK(part * a.hd + at, 4, n_rows * a.chunks * a.hd))
+        *reinterpret_cast<float4*>(a.part_o + part * a.hd + at) = v;
+      if (d == 0 && FRT_IDX_OK(part + row, n_rows * a.chunks)) {
+        float top = merge_m[r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_m[w * R + r]);
+        a.part_ml[part + row] = make_float2(top, sum);
+      }
+    }
+  }
+}
+
+// The chunks' parts of one query row joined: thread groups of hd / 4 lanes take
+// every other chunk, in a fixed order.
+constexpr int kJoinThreads = 256;
+template <int R>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
+  __shared__ float4 sums[kJoinThreads];
+  const int b = blockIdx.y;
+  int x = blockIdx.x;
+  const int r = x % R;
+  x /= R;
+  const int kvh = x % a.Hkv;
+  const int rt = x / a.Hkv;
+  pdl_enter();
+  const Rows rows = query_rows<R>(a, b, rt, kvh);
+  const int tok = __shfl_sync(0xFFFFFFFFu, rows.tok, r), head = __shfl_sync(0xFFFFFFFFu, rows.head, r);
+  const int n = (rows.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+  if (tok < 0 || n <= 1) return;
+  const int64_t n_rows = (int64_t)a.M * a.Hq, row = (int64_t)tok * a.Hq + head;
+  const float kInf = __int_as_float(0x7F800000);
+  const int lane = threadIdx.x & 31;
+  float top = -kInf;
+  for (int i = lane; i < n; i += 32)
+    if (FRT_IDX_OK(i * n_rows + row, n_rows * a.chunks)) top = fmaxf(top, a.part_ml[i * n_rows + row].x);
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  float sum = 0.0f;
+  for (int i = lane; i < n; i += 32)
+    if (FRT_IDX_OK(i * n_rows + row, n_rows * a.chunks)) {
+      const float2 ml = a.part_ml[i * n_rows + row];
+      sum += ml.y * (ml.x == -kInf ? 0.0f : ex2_approx(ml.x - top));
+    }
+  sum = group_sum<32>(sum);
+
+  const int lanes = a.hd / 4;
+  const int groups = kJoinThreads / lanes;
+  const int grp = threadIdx.x / lanes, d = (threadIdx.x - grp * lanes) * 4;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (grp < groups) {
+#pragma unroll 4
+    for (int i = grp; i < n; i += groups) {
+      const int64_t at = (i * n_rows + row) * a.hd + d;
+      if (!FRT_SPAN_OK(at, 4, n_rows * a.chunks * a.hd)) continue;
+      const float mx = a.part_ml[i * n_rows + row].x;
+      const float f = mx == -kInf ? 0.0f : ex2_approx(mx - top);
+      const float4 u = *reinterpret_cast<const float4*>(a.part_o + at);
+      v.x += u.x * f;
+      v.y += u.y * f;
+      v.z += u.z * f;
+      v.w += u.w * f;
+    }
+  }
+  sums[threadIdx.x] = v;
+  __syncthreads();
+  if (grp != 0) return;
+  for (int i = 1; i < groups; ++i) {
+    const float4 u = sums[i * lanes + threadIdx.x];
+    v.x += u.x;
+    v.y += u.y;
+    v.z += u.z;
+    v.w += u.w;
+  }
+  const float f = sum == 0.0f ? 0.0f : __ldg(a.kv_scales + 1) / sum;
+  const uint2 w = a.dt == FRT_F16 ? make_uint2(Pack16<FRT_F16>::from_float2(v.x * f, v.y * f),
+                                               Pack16<FRT_F16>::from_float2(v.z * f, v.w * f))
+                                  : make_uint2(Pack16<FRT_BF16>::from_float2(v.x * f, v.y * f),
+                                               Pack16<FRT_BF16>::from_float2(v.z * f, v.w * f));
+  if (FRT_SPAN_OK(row * a.hd + d, 4, n_rows * a.hd))
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.hd + d) = w;
+}
+
+// How a call is cut: NT x 8 query rows to a CTA, and the keys into chunks.
+struct Plan {
+  int nt, row_tiles, chunks, chunk_tiles;
+};
+Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
+  Plan p;
+  const int64_t rows = (int64_t)max_q_len * (Hq / Hkv);
+  p.nt = rows <= 8 ? 1 : rows <= 16 || hd > 128 ? 2 : 4;
+  const int64_t row_tiles = (rows + 8 * p.nt - 1) / (8 * p.nt);
+  p.row_tiles = (int)(row_tiles > 0x7FFFFFFF ? 0x7FFFFFFF : row_tiles);
+  const int64_t tiles = ((int64_t)max_kv_len + 3) / kTile + 1;
+  const int64_t ctas = row_tiles * Hkv * n_seqs;
+  // enough CTAs for one full wave; a batch of sequences, whose lengths
+  // differ, gets four
+  const int64_t want = (int64_t)kSMs * 4 * (n_seqs > 1 ? 4 : 1);
+  int64_t chunks = want / (ctas > 0 ? ctas : 1);
+  chunks = chunks < 1 ? 1 : chunks;
+  int64_t per = (tiles + chunks - 1) / chunks;
+  per = (per + kWarps - 1) / kWarps * kWarps;
+  p.chunk_tiles = (int)per;
+  p.chunks = (int)((tiles + per - 1) / per);
+  return p;
+}
+
+bool plan_args_ok(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
+  return M >= 0 && n_seqs > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && hd > 0 && hd % 16 == 0 && max_q_len > 0 &&
+         max_kv_len >= 0;
+}
+
+template <int HD, bool EXACT, int NT>
+frt_status launch_attn(const Args& a, cudaStream_t stream) {
+  using A = Attn<HD, EXACT, NT>;
+  static std::atomic<int> opted{48 * 1024};
+  const frt_status st = opt_in_smem(attn_kernel<HD, EXACT, NT>, A::kSmem, opted);
+  if (st != FRT_OK) return st;
+  const int64_t gx = (int64_t)a.Hkv * a.row_tiles * a.chunks;
+  if (gx > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
+  const frt_status s1 = launch(attn_kernel<HD, EXACT, NT>, dim3((unsigned)gx, a.n_seqs), dim3(kThreads), A::kSmem,
+                               stream, a);
+  if (s1 != FRT_OK || a.chunks == 1) return s1;
+  const int64_t jx = (int64_t)a.Hkv * a.row_tiles * A::R;
+  if (jx > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
+  return launch(join_kernel<A::R>, dim3((unsigned)jx, a.n_seqs), dim3(kJoinThreads), 0, stream, a);
+}
+template <int HD, int NT>
+frt_status launch_exact(const Args& a, cudaStream_t stream) {
+  return a.hd == HD ? launch_attn<HD, true, NT>(a, stream) : launch_attn<HD, false, NT>(a, stream);
+}
+template <int NT>
+frt_status launch_hd(const Args& a, cudaStream_t stream) {
+  if (a.hd <= 64) return launch_exact<64, NT>(a, stream);
+  if constexpr (NT <= 2) {
+    if (a.hd > 192) return launch_exact<256, NT>(a, stream);
+    if (a.hd > 128) return launch_exact<192, NT>(a, stream);
+  }
+  return launch_exact<128, NT>(a, stream);
+}
+
+}  // namespace
+}  // namespace frt
+
+using namespace frt;
+
+extern "C" size_t frt_attn_nvfp4_workspace_bytes(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len,
+                                                 int max_kv_len) {
+  if (!plan_args_ok(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len)) return 0;
+  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
+  if (p.chunks == 1) return 0;
+  return (size_t)p.chunks * M * Hq * (8 + 4 * (size_t)hd);
+}
+
+extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_codes, const uint8_t* k_sf,
+                                             const uint8_t* v_codes, const uint8_t* v_sf, const float* kv_scales,
+                                             const int32_t* kv_len, const int32_t* q_indptr,
+                                             const int32_t* page_table, void* out, void* workspace,
+                                             size_t workspace_bytes, int32_t* status, int M, int n_seqs, int Hq,
+                                             int Hkv, int hd, int capacity, int page_size, int max_pages,
+                                             int max_q_len, int max_kv_len, int window, float softmax_scale,
+                                             frt_dtype dt, cudaStream_t stream) {
+  if (!plan_args_ok(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len) || capacity <= 0 || !std::isfinite(softmax_scale) ||
+      !valid_dtype(dt))
+    return FRT_ERR_INVALID_ARG;
+  if (page_table != nullptr && (page_size <= 0 || page_size % 4 != 0 || max_pages < 0)) return FRT_ERR_INVALID_ARG;
+  if (q_indptr == nullptr && n_seqs != 1) return FRT_ERR_INVALID_ARG;
+  if (hd > 256 || n_seqs > 65535 || max_kv_len > 0x7FFFFF00) return FRT_ERR_UNSUPPORTED;
+  if (M == 0) return FRT_OK;
+  for (const void* p : {q, (const void*)k_codes, (const void*)k_sf, (const void*)v_codes, (const void*)v_sf,
+                        (const void*)out})
+    if (p == nullptr || !aligned(p, 16)) return FRT_ERR_INVALID_ARG;
+  if (kv_scales == nullptr || !aligned(kv_scales, 4) || kv_len == nullptr || !aligned(kv_len, 4) ||
+      !aligned(q_indptr, 4) || !aligned(page_table, 4) || !aligned(status, 4))
+    return FRT_ERR_INVALID_ARG;
+  const size_t need = frt_attn_nvfp4_workspace_bytes(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
+    return FRT_ERR_INVALID_ARG;
+  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
+  Args a = {};
+  a.q = q;
+  a.k_codes = k_codes;
+  a.k_sf = k_sf;
+  a.v_codes = v_codes;
+  a.v_sf = v_sf;
+  a.kv_scales = kv_scales;
+  a.kv_len = kv_len;
+  a.q_indptr = q_indptr;
+  a.page_table = page_table;
+  a.out = out;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.chunks * M * Hq * hd);
+  a.status = status;
+  a.M = M;
+  a.n_seqs = n_seqs;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.hd = hd;
+  a.group = Hq / Hkv;
+  a.capacity = capacity;
+  a.max_q_len = max_q_len;
+  a.max_len = max_kv_len < capacity ? max_kv_len : capacity;
+  if (page_table != nullptr) {
+    const int64_t holds = (int64_t)max_pages * page_size;
+    a.max_len = (int)(holds < max_kv_len ? holds : max_kv_len);
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.n_pages = capacity / page_size;
+    // floor(p / d) = (p + umulhi(p, mul)) >> shift with 2^shift >= d,
+    // mul = floor(2^32 (2^shift - d) / d) + 1, for every 0 <= p < 2^31
+    while ((1LL << a.page_shift) < page_size) ++a.page_shift;
+    a.page_mul = (uint32_t)((((1ULL << a.page_shift) - page_size) << 32) / page_size + 1);
+  }
+  a.window = window;
+  a.row_tiles = p.row_tiles;
+  a.chunks = p.chunks;
+  a.chunk_tiles = p.chunk_tiles;
+  a.scale_log2 = softmax_scale * kLog2e;
+  a.dt = dt;
+  return p.nt == 1 ? launch_hd<1>(a, stream) : p.nt == 2 ? launch_hd<2>(a, stream) : launch_hd<4>(a, stream);
+}
