@@ -29,6 +29,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfrt.so")
 DEBUG_LIB_PATH = os.path.join(_HERE, "libfrt_debug.so")
+MARSHAL_PATH = os.path.join(_HERE, "_marshal.so")
 
 FRT_OK, FRT_ERR_INVALID_ARG, FRT_ERR_UNSUPPORTED, FRT_ERR_CUDA = 0, 1, 2, 3
 DTYPE = {torch.float16: 0, torch.bfloat16: 1}
@@ -41,8 +42,9 @@ EXPORTS = ("frt_residual_rmsnorm_fp8", "frt_qkv_norm_rope_kvcache", "frt_gate_ac
            "frt_qkv_layernorm_rope_kvcache",
            "frt_residual_rmsnorm_nvfp4", "frt_gate_act_nvfp4", "frt_qkv_norm_rope_prepq_kvcache",
            "frt_gate_residual_adarms_fp8", "frt_qkv_norm_rope_nvfp4_kvcache", "frt_nvfp4_kvcache_read",
-           "frt_attn_nvfp4_workspace_bytes", "frt_attn_nvfp4_kvcache", "frt_matvec_nvfp4", "frt_noop", "frt_copy_rows", "frt_set_pdl", "frt_get_pdl", "frt_set_wait_polls",
-           "frt_get_wait_polls", "frt_status_string")
+           "frt_attn_nvfp4_workspace_bytes", "frt_attn_nvfp4_kvcache", "frt_matvec_nvfp4", "frt_noop",
+           "frt_copy_rows", "frt_set_pdl", "frt_get_pdl", "frt_set_wait_polls", "frt_get_wait_polls",
+           "frt_status_string")
 
 
 class FrtError(RuntimeError):
@@ -152,6 +154,8 @@ def _open(path):
     L.frt_get_wait_polls.restype = i32
     L.frt_status_string.argtypes = [i32]
     L.frt_status_string.restype = c.c_char_p
+    # for the native marshalling of the NVFP4 operators (csrc/marshal.cpp)
+    L.addresses = {n: c.cast(getattr(L, n), vp).value for n in EXPORTS}
     return L
 
 
@@ -178,20 +182,6 @@ def _stream(stream):
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _dtype(fn, t):
-    if t.dtype not in DTYPE:
-        raise FrtError(fn, FRT_ERR_INVALID_ARG, "%s is not a supported 16-bit type" % t.dtype)
-    return DTYPE[t.dtype]
-
-
-def _device_of(t):
-    """Context in which t's device is the current one (its own current stream
-    included)."""
-    if not t.is_cuda:
-        raise FrtError("marshal", FRT_ERR_INVALID_ARG, "tensor is not on a CUDA device")
-    return torch.cuda.device(t.device) if t.device.index != torch.cuda.current_device() else contextlib.nullcontext()
 
 
 def frt_residual_rmsnorm_fp8(x, residual_in, residual_out, weight, out_fp8, static_scale=None,
@@ -364,33 +354,22 @@ def nvfp4_kv_sf_shape(capacity, Hkv, hd):
     return ((capacity + 3) // 4, Hkv, hd // 16, 4)
 
 
-def _shape(fn, name, t, want):
-    if t is not None and tuple(t.shape) != tuple(want):
-        raise FrtError(fn, FRT_ERR_INVALID_ARG, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(want)))
+_native = None
 
 
-def _type(fn, name, t, *want):
-    if t is not None and t.dtype not in want:
-        raise FrtError(fn, FRT_ERR_INVALID_ARG, "%s is %s, expected %s" % (name, t.dtype, want[0]))
-
-
-def _same_device(fn, first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise FrtError(fn, FRT_ERR_INVALID_ARG, "tensors on %s and %s" % (first.device, t.device))
-
-
-def _kv_cache_args(fn, k_codes, k_sf, v_codes, v_sf, kv_scales, Hkv, hd):
-    """Checks the five tensors of an NVFP4 KV cache; returns its capacity."""
-    capacity = k_codes.shape[0]
-    for name, codes, sf in (("k", k_codes, k_sf), ("v", v_codes, v_sf)):
-        _type(fn, name + "_codes", codes, torch.uint8)
-        _type(fn, name + "_sf", sf, torch.uint8)
-        _shape(fn, name + "_codes", codes, (capacity, Hkv, hd // 2))
-        _shape(fn, name + "_sf", sf, nvfp4_kv_sf_shape(capacity, Hkv, hd))
-    _type(fn, "kv_scales", kv_scales, torch.float32)
-    _shape(fn, "kv_scales", kv_scales, (2,))
-    return capacity
+def _entry(name):
+    """(marshalling module, address of a C entry point, address of
+    frt_status_string) of the library in use."""
+    global _native
+    if _native is None:
+        if not os.path.exists(MARSHAL_PATH):
+            raise FrtError("load", -1, "%s is missing; build it with `python -m memory_bound_non_b200.build`" %
+                           MARSHAL_PATH)
+        from . import _marshal as module
+        module.set_error(FrtError)
+        _native = module
+    addresses = load().addresses
+    return _native, addresses[name], addresses["frt_status_string"]
 
 
 def frt_qkv_norm_rope_nvfp4_kvcache(qkv, q_norm_w, k_norm_w, cos_tab, sin_tab, positions, q_out, k_codes, k_sf,
@@ -399,49 +378,16 @@ def frt_qkv_norm_rope_nvfp4_kvcache(qkv, q_norm_w, k_norm_w, cos_tab, sin_tab, p
     """Op (b) with an NVFP4 KV cache: codes uint8 [capacity, Hkv, hd/2], sf uint8
     nvfp4_kv_sf_shape(capacity, Hkv, hd), kv_scales fp32[2] (global scales of K
     and V).  slots int32 [M] (-1: skip the row) or None (slot = position)."""
-    fn = "frt_qkv_norm_rope_nvfp4_kvcache"
-    M = qkv.shape[0]
-    capacity = _kv_cache_args(fn, k_codes, k_sf, v_codes, v_sf, kv_scales, Hkv, hd)
-    _shape(fn, "qkv", qkv, (M, (Hq + 2 * Hkv) * hd))
-    _shape(fn, "q_out", q_out, (M, Hq, hd))
-    _type(fn, "q_out", q_out, qkv.dtype)
-    for name, w in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w)):
-        _type(fn, name, w, qkv.dtype)
-        _shape(fn, name, w, (hd,))
-    for name, t in (("cos_tab", cos_tab), ("sin_tab", sin_tab)):
-        _type(fn, name, t, torch.float32)
-        _shape(fn, name, t, (cos_tab.shape[0], hd // 2))
-    for name, t in (("positions", positions), ("slots", slots)):
-        _type(fn, name, t, torch.int32)
-        _shape(fn, name, t, (M,))
-    _type(fn, "status", status, torch.int32)
-    _same_device(fn, qkv, q_norm_w, k_norm_w, cos_tab, sin_tab, positions, slots, q_out, k_codes, k_sf, v_codes, v_sf,
-                 kv_scales, status)
-    with _device_of(qkv):
-        st = load().frt_qkv_norm_rope_nvfp4_kvcache(
-            _ptr(qkv), _ptr(q_norm_w), _ptr(k_norm_w), _ptr(cos_tab), _ptr(sin_tab), _ptr(positions), _ptr(slots),
-            _ptr(q_out), _ptr(k_codes), _ptr(k_sf), _ptr(v_codes), _ptr(v_sf), _ptr(kv_scales), _ptr(status), M, Hq,
-            Hkv, hd, cos_tab.shape[0], capacity, float(eps), _dtype(fn, qkv), _stream(stream))
-    _check(fn, st)
+    m, fn, text = _entry("frt_qkv_norm_rope_nvfp4_kvcache")
+    m.write(fn, text, qkv, q_norm_w, k_norm_w, cos_tab, sin_tab, positions, slots, q_out, k_codes, k_sf, v_codes, v_sf,
+            kv_scales, status, Hq, Hkv, hd, eps, stream)
 
 
 def frt_nvfp4_kvcache_read(k_codes, k_sf, v_codes, v_sf, kv_scales, slots, k_out, v_out, status=None, stream=None):
     """Slots of an NVFP4 KV cache back in 16 bits: k_out, v_out [n, Hkv, hd];
     slots int32 [n] or None (slots 0 .. n-1)."""
-    fn = "frt_nvfp4_kvcache_read"
-    n, Hkv, hd = k_out.shape
-    capacity = _kv_cache_args(fn, k_codes, k_sf, v_codes, v_sf, kv_scales, Hkv, hd)
-    _shape(fn, "v_out", v_out, k_out.shape)
-    _type(fn, "v_out", v_out, k_out.dtype)
-    _type(fn, "slots", slots, torch.int32)
-    _shape(fn, "slots", slots, (n,))
-    _type(fn, "status", status, torch.int32)
-    _same_device(fn, k_out, v_out, k_codes, k_sf, v_codes, v_sf, kv_scales, slots, status)
-    with _device_of(k_out):
-        st = load().frt_nvfp4_kvcache_read(
-            _ptr(k_codes), _ptr(k_sf), _ptr(v_codes), _ptr(v_sf), _ptr(kv_scales), _ptr(slots), _ptr(k_out),
-            _ptr(v_out), _ptr(status), n, Hkv, hd, capacity, _dtype(fn, k_out), _stream(stream))
-    _check(fn, st)
+    m, fn, text = _entry("frt_nvfp4_kvcache_read")
+    m.read(fn, text, k_codes, k_sf, v_codes, v_sf, kv_scales, slots, k_out, v_out, status, stream)
 
 
 def attn_nvfp4_workspace(q, Hkv, max_kv_len, n_seqs=1, max_q_len=None):
@@ -449,7 +395,7 @@ def attn_nvfp4_workspace(q, Hkv, max_kv_len, n_seqs=1, max_q_len=None):
     q's device (None where the call needs none).  Calls that may run at the
     same time need one each."""
     M, Hq, hd = q.shape
-    n = load().frt_attn_nvfp4_workspace_bytes(M, n_seqs, Hq, Hkv, hd, M if max_q_len is None else max_q_len,
+    n = load().frt_attn_nvfp4_workspace_bytes(M, n_seqs, Hq, Hkv, hd, max(M, 1) if max_q_len is None else max_q_len,
                                               max_kv_len)
     return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
 
@@ -464,43 +410,10 @@ def frt_attn_nvfp4_kvcache(q, k_codes, k_sf, v_codes, v_sf, kv_scales, kv_len, o
     the tokens of a sequence and kv_len (defaults: M, and what the cache or the
     page table holds).  workspace: from attn_nvfp4_workspace (None: allocated
     for the call)."""
-    fn = "frt_attn_nvfp4_kvcache"
-    M, Hq, hd = q.shape
-    Hkv = k_codes.shape[1]
-    capacity = _kv_cache_args(fn, k_codes, k_sf, v_codes, v_sf, kv_scales, Hkv, hd)
-    _shape(fn, "out", out, q.shape)
-    _type(fn, "out", out, q.dtype)
-    _type(fn, "kv_len", kv_len, torch.int32)
-    _shape(fn, "kv_len", kv_len, (M,))
-    _type(fn, "q_indptr", q_indptr, torch.int32)
-    _type(fn, "page_table", page_table, torch.int32)
-    _type(fn, "status", status, torch.int32)
-    n_seqs, max_pages = 1, 0
-    if q_indptr is not None:
-        n_seqs = q_indptr.numel() - 1
-    if page_table is not None:
-        max_pages = page_table.shape[-1]
-        _shape(fn, "page_table", page_table, (n_seqs, max_pages))
-    if max_q_len is None:
-        max_q_len = max(M, 1)
-    if max_kv_len is None:
-        max_kv_len = capacity if page_table is None else max_pages * page_size
-    _same_device(fn, q, k_codes, k_sf, v_codes, v_sf, kv_scales, kv_len, out, q_indptr, page_table, workspace, status)
-    with _device_of(q):
-        if workspace is None:
-            # allocated on the launching stream, so that its memory is reused only behind this call
-            if stream is None:
-                workspace = attn_nvfp4_workspace(q, Hkv, max_kv_len, n_seqs, max_q_len)
-            else:
-                with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=q.device)):
-                    workspace = attn_nvfp4_workspace(q, Hkv, max_kv_len, n_seqs, max_q_len)
-        st = load().frt_attn_nvfp4_kvcache(
-            _ptr(q), _ptr(k_codes), _ptr(k_sf), _ptr(v_codes), _ptr(v_sf), _ptr(kv_scales), _ptr(kv_len),
-            _ptr(q_indptr), _ptr(page_table), _ptr(out), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status), M, n_seqs, Hq,
-            Hkv, hd, capacity, page_size, max_pages, max_q_len, max_kv_len, window, float(softmax_scale),
-            _dtype(fn, q), _stream(stream))
-    _check(fn, st)
+    m, fn, text = _entry("frt_attn_nvfp4_kvcache")
+    m.attend(fn, text, _lib.addresses["frt_attn_nvfp4_workspace_bytes"], q, k_codes, k_sf, v_codes, v_sf, kv_scales,
+             kv_len, q_indptr, page_table, out, workspace, status, window, page_size, max_q_len, max_kv_len,
+             softmax_scale, stream)
 
 
 X_FORMAT = {"16": 0, "e4m3": 1, "e4m3_block": 2, "nvfp4": 3}
@@ -512,33 +425,12 @@ def frt_matvec_nvfp4(x, w_codes, w_sf, w_scale, y, bias=None, x_format="16", x_s
     sf_layout, w_scale fp32[1]).  x: 16-bit [M, K]; "e4m3" / "e4m3_block" uint8
     [M, K] with x_scales fp32 [1] / [M, ceil(K/128)]; "nvfp4" uint8 [M, K/2] with
     x_sf in sf_layout and x_scales fp32[1]."""
-    fn = "frt_matvec_nvfp4"
-    M, N = y.shape
-    K = 2 * w_codes.shape[1]
+    m, fn, text = _entry("frt_matvec_nvfp4")
     if x_format not in X_FORMAT or sf_layout not in SF_LAYOUT:
-        raise FrtError(fn, FRT_ERR_INVALID_ARG, "unknown x_format %r or sf_layout %r" % (x_format, sf_layout))
-    _type(fn, "x", x, y.dtype if x_format == "16" else torch.uint8)
-    _shape(fn, "x", x, (M, K // 2 if x_format == "nvfp4" else K))
-    for name, t, rows in (("w_sf", w_sf, N), ("x_sf", x_sf if x_format == "nvfp4" else None, M)):
-        _type(fn, name, t, torch.uint8)
-        if t is not None and t.numel() != nvfp4_sf_bytes(rows, K, sf_layout):
-            raise FrtError(fn, FRT_ERR_INVALID_ARG, "%s holds %d bytes, expected %d" % (
-                name, t.numel(), nvfp4_sf_bytes(rows, K, sf_layout)))
-    _type(fn, "w_codes", w_codes, torch.uint8)
-    _shape(fn, "w_codes", w_codes, (N, K // 2))
-    _type(fn, "w_scale", w_scale, torch.float32)
-    _shape(fn, "w_scale", w_scale, (1,))
-    if x_format != "16":
-        _type(fn, "x_scales", x_scales, torch.float32)
-        _shape(fn, "x_scales", x_scales, (M, (K + 127) // 128) if x_format == "e4m3_block" else (1,))
-    _type(fn, "bias", bias, y.dtype)
-    _shape(fn, "bias", bias, (N,))
-    _same_device(fn, y, x, w_codes, w_sf, w_scale, bias, x_scales, x_sf)
-    with _device_of(y):
-        st = load().frt_matvec_nvfp4(_ptr(x), _ptr(x_scales), _ptr(x_sf), _ptr(w_codes), _ptr(w_sf), _ptr(w_scale),
-                                     _ptr(bias), _ptr(y), M, N, K, X_FORMAT[x_format], SF_LAYOUT[sf_layout],
-                                     _dtype(fn, y), _stream(stream))
-    _check(fn, st)
+        raise FrtError("frt_matvec_nvfp4", FRT_ERR_INVALID_ARG,
+                       "unknown x_format %r or sf_layout %r" % (x_format, sf_layout))
+    m.matvec(fn, text, x, x_scales, x_sf, w_codes, w_sf, w_scale, bias, y, X_FORMAT[x_format], SF_LAYOUT[sf_layout],
+             stream)
 
 
 def frt_set_pdl(enable: bool):

@@ -1,8 +1,9 @@
-"""Build libfrt.so (the CUDA library) in-tree for sm_100a with nvcc, and its
+"""Build libfrt.so (the CUDA library) in-tree for sm_100a with nvcc, its
 bounds-checked variant libfrt_debug.so (FRT_DEBUG_BOUNDS, relocatable device
-code so that every source shares one device-side violation counter).
+code so that every source shares one device-side violation counter), and
+_marshal.so (the binding's native argument marshalling, g++ against torch).
 
-    python -m memory_bound_non_b200.build        # build both if sources changed
+    python -m memory_bound_non_b200.build        # build all if sources changed
     python -m memory_bound_non_b200.build -f     # force
 """
 import concurrent.futures
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfrt.so")
 DEBUG_LIB = os.path.join(PKG, "libfrt_debug.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL_LIB = os.path.join(PKG, "_marshal.so")
 DEBUG_FLAGS = ["-rdc=true", "-DFRT_DEBUG_BOUNDS"]
 
 NVCC_FLAGS = [
@@ -83,12 +87,35 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     return lib
 
 
+def build_marshal(force: bool = False) -> str:
+    """Compile _marshal.so against the installed torch and CUDA headers."""
+    deps = [MARSHAL_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(MARSHAL_LIB) and \
+            all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL_LIB) for d in deps):
+        return MARSHAL_LIB
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    nvcc = shutil.which(os.environ.get("NVCC", "nvcc"))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc))) if nvcc else "/usr/local/cuda"
+    include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include/torch/csrc/api/include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    tmp = MARSHAL_LIB + ".tmp.%d" % os.getpid()
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w"] +
+                   [a for d in include for a in ("-I", d)] + [MARSHAL_SRC, "-o", tmp,
+                    "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                    "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+                    "-ltorch_python"], check=True)
+    os.replace(tmp, MARSHAL_LIB)
+    return MARSHAL_LIB
+
+
 def build_all(force: bool = False, verbose: bool = False):
-    """Both libraries, built side by side (their objects are independent)."""
-    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as pool:
+    """The libraries, built side by side (their objects are independent)."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=3) as pool:
         release = pool.submit(build, force, verbose)
         debug = pool.submit(build, force, verbose, True)
-        return release.result(), debug.result()
+        marshal = pool.submit(build_marshal, force)
+        return release.result(), debug.result(), marshal.result()
 
 
 if __name__ == "__main__":

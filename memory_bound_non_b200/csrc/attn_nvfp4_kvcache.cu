@@ -177,22 +177,58 @@ struct Attn {
     return entry * a.page_size + (pos - page * a.page_size);
   }
 
-  static __device__ __forceinline__ void load_k(const Args& a, int kvh, int slot, int count, int t, KFrag& f) {
-    const int nblk = a.hd >> 4;
-    const int64_t row_bytes = (int64_t)a.Hkv * (a.hd >> 1);
-    const int64_t code0 = (int64_t)slot * row_bytes + (int64_t)kvh * (a.hd >> 1) + t * 8 * J;
-    const uint8_t* p = a.k_codes + code0;
-    const int64_t code_bytes = row_bytes * a.capacity;
+  // Where this lane's part of slot 0 lies; a slot's codes are row_bytes on, and
+  // the factors of the quad that begins with slot s are s * sf_row on.  Blocks
+  // behind hd (a build of a larger HD) are the last one again; K's factors are
+  // cleared there (k_keep), V's dimensions are not written.
+  struct Base {
+    const uint8_t* k;
+    const uint8_t* v;
+    const uint8_t* k_sf;
+    const uint8_t* v_sf;
+    int row_bytes, sf_row, last;
+    int k_off[J], v_off[J], v_sf_off[kVs];
+    uint32_t k_keep[J];
+    __device__ __forceinline__ Base(const Args& a, int kvh, int g, int t) {
+      const int nblk = a.hd >> 4;
+      k = a.k_codes + kvh * (a.hd >> 1);
+      v = a.v_codes + kvh * (a.hd >> 1);
+      k_sf = a.k_sf + kvh * nblk * 4;
+      v_sf = a.v_sf + kvh * nblk * 4;
+      row_bytes = a.Hkv * (a.hd >> 1);
+      sf_row = a.Hkv * nblk;
+      last = a.capacity - 1;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        k_off[j] = EXACT ? t * J + j : min(t * J + j, nblk - 1);
+        k_keep[j] = EXACT || t * J + j < nblk ? 0xFFFFFFFFu : 0u;
+        v_off[j] = EXACT ? g * J + j : min(g * J + j, 2 * nblk - 1);
+      }
+#pragma unroll
+      for (int j = 0; j < kVs; ++j) v_sf_off[j] = v_off[J == 3 ? j : 2 * j] >> 1;
+    }
+  };
+  static __device__ __forceinline__ bool code_ok(const Args& a, const uint8_t* p, const uint8_t* base, int bytes) {
+    return FRT_SPAN_OK(p - base, bytes, (int64_t)a.capacity * a.Hkv * (a.hd >> 1));
+  }
+  static __device__ __forceinline__ bool sf_ok(const Args& a, const uint8_t* p, const uint8_t* base) {
+    return FRT_SPAN_OK(p - base, 4, (int64_t)((a.capacity + 3) >> 2) * a.Hkv * (a.hd >> 4) * 4);
+  }
+
+  // The four slots from `slot` on.  Every load is made: a quad that is not
+  // there (slot < 0) is slot 0, slots behind the capacity are the last one;
+  // what they bring is masked by position later.
+  static __device__ __forceinline__ void load_k(const Args& a, const Base& base, int slot, KFrag& f) {
+    const int s0 = max(slot, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool on = slot >= 0 && i < count;
-      const uint8_t* pi = p + i * row_bytes;
+      const uint8_t* p = base.k + (int64_t)min(s0 + i, base.last) * base.row_bytes;
       if (EXACT && (J & 1) == 0) {
+        p += 8 * base.k_off[0];
 #pragma unroll
         for (int j = 0; j < J; j += 2) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (on && FRT_SPAN_OK(code0 + i * row_bytes + 8 * j, 16, code_bytes))
-            v = ld_stream(reinterpret_cast<const uint4*>(pi + 8 * j));
+          if (code_ok(a, p + 8 * j, a.k_codes, 16)) v = ld_stream(reinterpret_cast<const uint4*>(p + 8 * j));
           f.c[i][2 * j] = v.x;
           f.c[i][2 * j + 1] = v.y;
           f.c[i][2 * j + 2] = v.z;
@@ -201,78 +237,62 @@ struct Attn {
       } else {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
+          const uint8_t* pj = p + (EXACT ? 8 * base.k_off[0] + 8 * j : 8 * base.k_off[j]);
           uint2 v = make_uint2(0, 0);
-          if (on && (EXACT || t * J + j < nblk) && FRT_SPAN_OK(code0 + i * row_bytes + 8 * j, 8, code_bytes))
-            v = ld_stream(reinterpret_cast<const uint2*>(pi + 8 * j));
+          if (code_ok(a, pj, a.k_codes, 8)) v = ld_stream(reinterpret_cast<const uint2*>(pj));
           f.c[i][2 * j] = v.x;
           f.c[i][2 * j + 1] = v.y;
         }
       }
     }
-    const int64_t word0 = ((int64_t)(slot >> 2) * a.Hkv + kvh) * nblk + t * J;
-    const int64_t words = (int64_t)((a.capacity + 3) >> 2) * a.Hkv * nblk;
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(a.k_sf);
+    const uint8_t* s = base.k_sf + (int64_t)s0 * base.sf_row;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
+      const uint8_t* sj = s + (EXACT ? 4 * base.k_off[0] + 4 * j : 4 * base.k_off[j]);
       f.sf[j] = 0;
-      if (slot >= 0 && (EXACT || t * J + j < nblk) && FRT_IDX_OK(word0 + j, words)) f.sf[j] = __ldg(s + word0 + j);
+      if (sf_ok(a, sj, a.k_sf)) f.sf[j] = __ldg(reinterpret_cast<const uint32_t*>(sj));
     }
   }
 
-  // Slots of quad 0 (slot0) and 1 (slot1), `count` valid slots in each.
-  static __device__ __forceinline__ void load_v(const Args& a, int kvh, int slot0, int slot1, int count0, int count1,
-                                                int g, VFrag& f) {
-    const int nblk = a.hd >> 4;
-    const int64_t row_bytes = (int64_t)a.Hkv * (a.hd >> 1);
-    const int64_t code_bytes = row_bytes * a.capacity;
-    const int64_t words = (int64_t)((a.capacity + 3) >> 2) * a.Hkv * nblk;
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(a.v_sf);
+  // Half h of a lane's slots: the quad from `slot` on, as load_k.
+  static __device__ __forceinline__ void load_v(const Args& a, const Base& base, int h, int slot, VFrag& f) {
+    const int s0 = max(slot, 0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int slot = h == 0 ? slot0 : slot1;
-      const int count = h == 0 ? count0 : count1;
-      const int64_t code0 = (int64_t)slot * row_bytes + (int64_t)kvh * (a.hd >> 1) + g * 4 * J;
-      const uint8_t* p = a.v_codes + code0;
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* p = base.v + (int64_t)min(s0 + i, base.last) * base.row_bytes;
+      if (J == 4 && EXACT) {
+        p += 4 * base.v_off[0];
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (code_ok(a, p, a.v_codes, 16)) v = ld_stream(reinterpret_cast<const uint4*>(p));
+        f.c[h][i][0] = v.x;
+        f.c[h][i][1 % J] = v.y;
+        f.c[h][i][2 % J] = v.z;
+        f.c[h][i][3 % J] = v.w;
+      } else if ((J & 1) == 0) {
+        // (hd / 8 is even, so a clamped pair begins at hd / 8 - 2)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool on = slot >= 0 && i < count;
-        const uint8_t* pi = p + i * row_bytes;
-        const int64_t at = code0 + i * row_bytes;
-        if (J == 4 && EXACT) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (on && FRT_SPAN_OK(at, 16, code_bytes)) v = ld_stream(reinterpret_cast<const uint4*>(pi));
-          f.c[h][i][0] = v.x;
-          f.c[h][i][1 % J] = v.y;
-          f.c[h][i][2 % J] = v.z;
-          f.c[h][i][3 % J] = v.w;
-        } else if ((J & 1) == 0) {
+        for (int j = 0; j < J; j += 2) {
+          const uint8_t* pj = p + (EXACT ? 4 * base.v_off[0] + 4 * j : 4 * (base.v_off[j] & ~1));
+          uint2 v = make_uint2(0, 0);
+          if (code_ok(a, pj, a.v_codes, 8)) v = ld_stream(reinterpret_cast<const uint2*>(pj));
+          f.c[h][i][j] = v.x;
+          f.c[h][i][(j + 1) % J] = v.y;
+        }
+      } else {
 #pragma unroll
-          for (int j = 0; j < J; j += 2) {
-            uint2 v = make_uint2(0, 0);
-            if (on && (EXACT || g * J + j < 2 * nblk) && FRT_SPAN_OK(at + 4 * j, 8, code_bytes))
-              v = ld_stream(reinterpret_cast<const uint2*>(pi + 4 * j));
-            f.c[h][i][j] = v.x;
-            f.c[h][i][(j + 1) % J] = v.y;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            f.c[h][i][j] = 0;
-            if (on && (EXACT || g * J + j < 2 * nblk) && FRT_SPAN_OK(at + 4 * j, 4, code_bytes))
-              f.c[h][i][j] = __ldg(reinterpret_cast<const uint32_t*>(pi + 4 * j));
-          }
+        for (int j = 0; j < J; ++j) {
+          const uint8_t* pj = p + (EXACT ? 4 * base.v_off[0] + 4 * j : 4 * base.v_off[j]);
+          f.c[h][i][j] = 0;
+          if (code_ok(a, pj, a.v_codes, 4)) f.c[h][i][j] = __ldg(reinterpret_cast<const uint32_t*>(pj));
         }
       }
-      // factors of slots behind the end may hold anything: cleared
-      const uint32_t keep = count >= 4 ? 0xFFFFFFFFu : (1u << (8 * max(count, 0))) - 1;
-      const int64_t word0 = ((int64_t)(slot >> 2) * a.Hkv + kvh) * nblk;
+    }
+    const uint8_t* s = base.v_sf + (int64_t)s0 * base.sf_row;
 #pragma unroll
-      for (int j = 0; j < kVs; ++j) {
-        const int blk = (g * J + (J == 3 ? j : 2 * j)) >> 1;
-        f.sf[h][j] = 0;
-        if (slot >= 0 && (EXACT || blk < nblk) && FRT_IDX_OK(word0 + blk, words))
-          f.sf[h][j] = __ldg(s + word0 + blk) & keep;
-      }
+    for (int j = 0; j < kVs; ++j) {
+      const uint8_t* sj = s + 4 * base.v_sf_off[j];
+      f.sf[h][j] = 0;
+      if (sf_ok(a, sj, a.v_sf)) f.sf[h][j] = __ldg(reinterpret_cast<const uint32_t*>(sj));
     }
   }
 
@@ -319,21 +339,21 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
   const float gs_k = __ldg(a.kv_scales), gs_v = __ldg(a.kv_scales + 1);
 
   // first loads, on their way while the queries are laid out
+  const typename A::Base base(a, kvh, g, t);
   typename A::KFrag kf;
   typename A::VFrag vf;
   int tile = tile0 + warp;
   auto position = [&](int tl) { return rows.first() + tl * kTile + 4 * g; };
   auto slot_of = [&](int tl) { return tl < tile1 ? A::quad_slot(a, b, position(tl), rows) : -1; };
-  auto fetch_k = [&](int tl, int slot) { A::load_k(a, kvh, slot, rows.all_hi - position(tl), t, kf); };
-  auto fetch_v = [&](int tl, int slot) {
-    const int s0 = __shfl_sync(0xFFFFFFFFu, slot, 8 * t), s1 = __shfl_sync(0xFFFFFFFFu, slot, 8 * t + 4);
-    const int left = rows.all_hi - (rows.first() + tl * kTile + 8 * t);
-    A::load_v(a, kvh, s0, s1, left, left - 4, g, vf);
+  auto fetch_k = [&](int slot) { A::load_k(a, base, slot, kf); };
+  auto fetch_v = [&](int slot) {
+    A::load_v(a, base, 0, __shfl_sync(0xFFFFFFFFu, slot, 8 * t), vf);
+    A::load_v(a, base, 1, __shfl_sync(0xFFFFFFFFu, slot, 8 * t + 4), vf);
   };
   int slot = slot_of(tile);
   int slot_next = slot_of(tile + kWarps);
-  fetch_k(tile, slot);
-  fetch_v(tile, slot);
+  fetch_k(slot);
+  fetch_v(slot);
 
   // queries: a warp a row, in the order that the lanes read them
   for (int r = warp; r < R; r += kWarps) {
@@ -399,8 +419,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
 #pragma unroll
     for (int jb = 0; jb < J; ++jb) {
       uint32_t sc[4];
-      e4m3x4_to_half2(__byte_perm(kf.sf[jb], 0, 0x1100), sc);
-      e4m3x4_to_half2(__byte_perm(kf.sf[jb], 0, 0x3322), sc + 2);
+      const uint32_t sf = EXACT ? kf.sf[jb] : kf.sf[jb] & base.k_keep[jb];
+      e4m3x4_to_half2(__byte_perm(sf, 0, 0x1100), sc);
+      e4m3x4_to_half2(__byte_perm(sf, 0, 0x3322), sc + 2);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         uint32_t h[4][4];
@@ -423,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
         }
       }
     }
-    fetch_k(tile + kWarps, slot_next);
+    fetch_k(slot_next);
 
     // ---- masks.  A NaN factor of V turns the weights of its slot NaN (for
     // the rows that see it) and counts as zero itself, so that it cannot reach
@@ -461,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[n][e] *= c[n][e & 1];
-    if (pos0 < rows.full_lo || pos0 + kTile > rows.full_hi || __any_sync(0xFFFFFFFFu, slot < 0)) {
+    if (pos0 < rows.full_lo || rows.full_hi - pos0 < kTile || __any_sync(0xFFFFFFFFu, slot < 0)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -549,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
         }
       }
     }
-    fetch_v(tile + kWarps, slot_next);
+    fetch_v(slot_next);
     slot = slot_next;
     slot_next = slot_after;
   }

@@ -65,56 +65,64 @@ __device__ __forceinline__ int64_t sf_bytes(const Args& a, int64_t n_rows) {
 // Weights of one group: rows g and g + 8, 32 codes and two factors each.
 struct WFrag {
   uint32_t c[2][4];
-  uint32_t sf;  // row g blocks 0, 1, row g + 8 blocks 0, 1
+  uint32_t sf[2];
 };
-// WIDE: K % 32 == 0, 16-byte loads of codes and 2-byte loads of factors.
-template <bool WIDE>
-__device__ __forceinline__ void load_w(const Args& a, int row0, int group, int g, int t, WFrag& f) {
-  f.sf = 0;
+// A lane's loads of an item (kItem groups): the item's start in rows g and g +
+// 8, and where its 32 codes of each group lie from there.  Every load is made:
+// rows behind the last are row N - 1 again, their sums are dropped; codes
+// behind K are the last ones again, x is zero there.
+// LAY: 0 any K, 1 K % 32 == 0 with row-major factors, 2 with swizzled ones;
+// K % 32 == 0 has 16-byte loads of codes and 2-byte loads of factors.
+template <int LAY>
+struct WLoader {
+  const uint8_t* c[2];
+  int row[2];
+  int col[kItem];  // first of the two 16-blocks, from the start of the row
+
+  __device__ __forceinline__ void set_rows(const Args& a, int row0, int g) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = row0 + g + 8 * h;
-    const int k = group * kGroup + 32 * t;
-    const int64_t at = (int64_t)row * (a.K >> 1) + (k >> 1);
-    const int64_t bytes = (int64_t)a.N * (a.K >> 1);
-    const int64_t n_sf = sf_bytes(a, a.N);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    uint32_t s = 0;
-    if (WIDE) {
-      if (row < a.N && k < a.K) {
-        const int64_t sa = sf_at(a, row, k >> 4);
-        if (FRT_SPAN_OK(at, 16, bytes)) v = ld_stream(reinterpret_cast<const uint4*>(a.w_codes + at));
-        if (FRT_SPAN_OK(sa, 2, n_sf)) s = __ldg(reinterpret_cast<const uint16_t*>(a.w_sf + sa));
-      }
-    } else {
-      if (row < a.N) {
-        if (k < a.K) {
-          const int64_t sa = sf_at(a, row, k >> 4);
-          if (FRT_SPAN_OK(at, 8, bytes)) {
-            const uint2 u = ld_stream(reinterpret_cast<const uint2*>(a.w_codes + at));
-            v.x = u.x;
-            v.y = u.y;
-          }
-          if (FRT_IDX_OK(sa, n_sf)) s = __ldg(a.w_sf + sa);
-        }
-        if (k + 16 < a.K) {
-          const int64_t sa = sf_at(a, row, (k >> 4) + 1);
-          if (FRT_SPAN_OK(at + 8, 8, bytes)) {
-            const uint2 u = ld_stream(reinterpret_cast<const uint2*>(a.w_codes + at + 8));
-            v.z = u.x;
-            v.w = u.y;
-          }
-          if (FRT_IDX_OK(sa, n_sf)) s |= (uint32_t)__ldg(a.w_sf + sa) << 8;
-        }
+    for (int h = 0; h < 2; ++h) {
+      row[h] = min(row0 + g + 8 * h, a.N - 1);
+      c[h] = a.w_codes + (int64_t)row[h] * (a.K >> 1);
+    }
+  }
+  __device__ __forceinline__ void set_item(const Args& a, int item, int t) {
+    const int last = (a.K >> 4) - (LAY == 0 ? 1 : 2);
+#pragma unroll
+    for (int u = 0; u < kItem; ++u) col[u] = min((item * kItem + u) * (kGroup / 16) + 2 * t, last);
+  }
+  __device__ __forceinline__ void load(const Args& a, int u, WFrag& f) const {
+    const int64_t bytes = (int64_t)a.N * (a.K >> 1), n_sf = sf_bytes(a, a.N);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* p = c[h] + 8 * col[u];
+      f.sf[h] = 0;
+      if (LAY == 0) {
+        const int next = min(col[u] + 1, (a.K >> 4) - 1);
+        const uint8_t* p1 = c[h] + 8 * next;
+        const int64_t s0 = sf_at(a, row[h], col[u]), s1 = sf_at(a, row[h], next);
+        uint2 v = make_uint2(0, 0), w = v;
+        if (FRT_SPAN_OK(p - a.w_codes, 8, bytes)) v = ld_stream(reinterpret_cast<const uint2*>(p));
+        if (FRT_SPAN_OK(p1 - a.w_codes, 8, bytes)) w = ld_stream(reinterpret_cast<const uint2*>(p1));
+        if (FRT_IDX_OK(s0, n_sf) && FRT_IDX_OK(s1, n_sf)) f.sf[h] = __ldg(a.w_sf + s0) | __ldg(a.w_sf + s1) << 8;
+        f.c[h][0] = v.x;
+        f.c[h][1] = v.y;
+        f.c[h][2] = w.x;
+        f.c[h][3] = w.y;
+      } else {
+        const int64_t s = LAY == 2 ? sf_offset_swizzled(row[h], col[u], a.K >> 4)
+                                   : (int64_t)row[h] * (a.K >> 4) + col[u];
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (FRT_SPAN_OK(p - a.w_codes, 16, bytes)) v = ld_stream(reinterpret_cast<const uint4*>(p));
+        if (FRT_SPAN_OK(s, 2, n_sf)) f.sf[h] = __ldg(reinterpret_cast<const uint16_t*>(a.w_sf + s));
+        f.c[h][0] = v.x;
+        f.c[h][1] = v.y;
+        f.c[h][2] = v.z;
+        f.c[h][3] = v.w;
       }
     }
-    f.c[h][0] = v.x;
-    f.c[h][1] = v.y;
-    f.c[h][2] = v.z;
-    f.c[h][3] = v.w;
-    f.sf |= s << (16 * h);
   }
-}
+};
 
 // Four elements of row r (0 based within the launch) at column k as two
 // binary16 pairs, and the factor of (row, group): a warp holds the 128 elements
@@ -158,13 +166,13 @@ __device__ __forceinline__ uint2 load_x4(const Args& a, int r, int k, float* sca
   return o;
 }
 
-template <int NT, int XF, bool WIDE>
+template <int NT, int XF, int LAY>
 __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int mr = NT == 1 ? min(a.rows, 8) : 8;  // rows of x that shared memory holds per 8
-  const int step_words = NT * mr * 4;           // uint2 words of 16 k
+  const int step_words = NT * mr * 4;           // 16-byte words of 32 k
   constexpr int kRed = NT * 8 * 17;             // a warp's sums, [row of x][weight row]
   float* red = reinterpret_cast<float*>(smem);
   uint2* xf = reinterpret_cast<uint2*>(smem + sizeof(float) * kWarps * kRed);
@@ -173,6 +181,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
   const int kw = a.kw, ks = warp & (kw - 1), rw = warp / kw, tiles_at_once = kWarps / kw;
   const int items = (a.groups + kItem - 1) / kItem;
   const bool one_seg = a.seg_items >= items;
+  // rows of x that are not there: the last one again, its sums are dropped
+  const uint4* x_lane = reinterpret_cast<const uint4*>(xf) + min(g, mr - 1) * 4 + t;
 
   // This warp's items: of each unit the items ks, ks + kw, ... of its weight
   // tile, unit after unit.
@@ -188,15 +198,12 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
     return c;
   };
   WFrag w[kItem];
-  auto fetch = [&](Cursor c, int u) {
-    const int group = c.item * kItem + u;
-    if (c.unit < a.units && group < a.groups)
-      load_w<WIDE>(a, (c.unit * tiles_at_once + rw) * 16, group, g, t, w[u]);
-  };
-  Cursor cur = {(int)blockIdx.x, ks};
-  if (ks >= items) cur.unit = a.units;  // (never: kw <= items)
+  WLoader<LAY> loader;
+  Cursor cur = {(int)blockIdx.x, ks};  // (kw <= items)
+  loader.set_rows(a, (cur.unit * tiles_at_once + rw) * 16, g);
+  loader.set_item(a, ks, t);
 #pragma unroll
-  for (int u = 0; u < kItem; ++u) fetch(cur, u);  // constant inputs: before the wait
+  for (int u = 0; u < kItem; ++u) loader.load(a, u, w[u]);  // constant inputs: before the wait
   const float w_scale = __ldg(a.w_scale);
   pdl_enter();
   const float scale = w_scale * (XF == kXE4M3 || XF == kXNvfp4 ? a.x_scales[0] : 1.0f);
@@ -215,13 +222,17 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
           const int r = i % rows, c = i / rows;
           float s;
           const uint2 v = load_x4<XF>(a, r, (seg * kItem + c) * kGroup + 4 * lane, &s);
-          xf[(c * 8 + (lane & 7)) * step_words + ((r >> 3) * mr + (r & 7)) * 4 + (lane >> 3)] = v;
+          // steps 2p and 2p + 1 of a lane side by side
+          const int pair = (lane & 7) >> 1;
+          xf[((c * 4 + pair) * step_words + ((r >> 3) * mr + (r & 7)) * 4 + (lane >> 3)) * 2 + (lane & 1)] = v;
           if (group_scaled(XF) && lane == 0) xs[c * (8 * NT) + r] = s;
         }
         __syncthreads();
       }
       while (cur.unit == unit && cur.item < seg_end) {
         const Cursor next = advance(cur);
+        if (next.unit != unit) loader.set_rows(a, (next.unit * tiles_at_once + rw) * 16, g);
+        loader.set_item(a, next.item, t);
 #pragma unroll
         for (int u = 0; u < kItem; ++u) {
           const int group = cur.item * kItem + u;
@@ -233,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
               for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.0f;
             }
             uint32_t sc[4];
-            e4m3x4_to_half2(__byte_perm(w[u].sf, 0, 0x1100), sc);
-            e4m3x4_to_half2(__byte_perm(w[u].sf, 0, 0x3322), sc + 2);
+            e4m3x4_to_half2(__byte_perm(w[u].sf[0], 0, 0x1100), sc);
+            e4m3x4_to_half2(__byte_perm(w[u].sf[1], 0, 0x1100), sc + 2);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {  // words of 8 codes
               uint32_t h0[4], h1[4];
@@ -245,16 +256,13 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
                 h0[e] = hmul2(h0[e], sc[q >> 1]);
                 h1[e] = hmul2(h1[e], sc[2 + (q >> 1)]);
               }
+              const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
+              const uint4* xb = x_lane + (c * 4 + q) * step_words;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t av[4] = {h0[2 * j], h1[2 * j], h0[2 * j + 1], h1[2 * j + 1]};
-                const uint2* xb = xf + (c * 8 + q * 2 + j) * step_words + g * 4 + t;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  uint2 bv = make_uint2(0, 0);
-                  if (NT > 1 || g < mr) bv = xb[n * 32];
-                  mma_16816(group_scaled(XF) ? part[n] : acc[n], av, bv.x, bv.y);
-                }
+              for (int n = 0; n < NT; ++n) {
+                const uint4 bv = xb[n * 32];
+                mma_16816(group_scaled(XF) ? part[n] : acc[n], a0, bv.x, bv.y);
+                mma_16816(group_scaled(XF) ? part[n] : acc[n], a1, bv.z, bv.w);
               }
             }
             if (group_scaled(XF)) {
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
                 }
             }
           }
-          fetch(next, u);
+          loader.load(a, u, w[u]);
         }
         cur = next;
       }
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
   }
 }
 
-template <int NT, int XF, bool WIDE>
+template <int NT, int XF, int LAY>
 frt_status launch_one(Args a, cudaStream_t stream) {
   const int items = (a.groups + kItem - 1) / kItem;
   a.kw = 1;
@@ -320,15 +328,16 @@ frt_status launch_one(Args a, cudaStream_t stream) {
   a.seg_items = (int)(seg < items ? seg : items);
   const size_t smem = red + a.seg_items * item_bytes;
   static std::atomic<int> opted{48 * 1024};
-  const frt_status st = opt_in_smem(matvec_kernel<NT, XF, WIDE>, smem, opted);
+  const frt_status st = opt_in_smem(matvec_kernel<NT, XF, LAY>, smem, opted);
   if (st != FRT_OK) return st;
   const int resident = kSMs * (NT <= 2 ? 2 : 1);
   const unsigned grid = (unsigned)(a.units < resident ? a.units : resident);
-  return launch(matvec_kernel<NT, XF, WIDE>, dim3(grid), dim3(kThreads), smem, stream, a);
+  return launch(matvec_kernel<NT, XF, LAY>, dim3(grid), dim3(kThreads), smem, stream, a);
 }
 template <int NT, int XF>
 frt_status launch_wide(const Args& a, cudaStream_t stream) {
-  return a.K % 32 == 0 ? launch_one<NT, XF, true>(a, stream) : launch_one<NT, XF, false>(a, stream);
+  if (a.K % 32 != 0) return launch_one<NT, XF, 0>(a, stream);
+  return a.swizzled ? launch_one<NT, XF, 2>(a, stream) : launch_one<NT, XF, 1>(a, stream);
 }
 template <int XF>
 frt_status launch_rows(Args a, cudaStream_t stream) {
