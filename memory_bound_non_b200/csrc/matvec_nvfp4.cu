@@ -9,14 +9,17 @@
 // = lane % 4 a lane holds weight rows g and g + 8 at k = 32 t .. 32 t + 31 of a
 // group of 128, one 16-byte load a row, and two factors a row.  A warp keeps
 // four groups of weights on their way (4 KB and their factors), which is what
-// covers the HBM latency; the KW warps of a CTA that share a weight tile split
-// k, and their sums are joined in shared memory in a fixed order.
+// covers the HBM latency.  Tiles are dealt to the CTAs in turn, so that the SMs'
+// shares differ by one tile at most; a warp takes a tile alone, or kw warps
+// split its k and join their sums in shared memory in a fixed order.
 //
-// x lies in shared memory as binary16 in the order in which the lanes read it.
-// FP16 rows, e4m3 codes and NVFP4 code * factor are exact there.  bf16 rows are
-// scaled by a power of two per row and group, and like the block-scaled FP8
-// rows keep a factor per row and group that is applied to the group's fp32
-// sums.
+// x lies in shared memory as binary16 in the order in which the lanes read it
+// (16 bytes are a lane's part of two products).  FP16 rows, e4m3 codes and
+// NVFP4 code * factor are exact there.  bf16 rows are scaled by a power of two
+// per row and group, and like the block-scaled FP8 rows keep a factor per row
+// and group that is applied to the group's fp32 sums.
+#include <algorithm>
+
 #include "frt_device.cuh"
 #include "frt_host.h"
 
@@ -25,15 +28,11 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kGroup = 128;   // k of one load
-constexpr int kItem = 4;      // groups a warp has on their way
+constexpr int kGroup = 128;  // k of one load
+constexpr int kAhead = 4;    // groups a warp has on their way
 constexpr int kSMs = 148;
-constexpr int kXBytes = 80 * 1024;  // of x in shared memory at a time
 
-// how x enters: 16-bit without a scale (f16), with a power of two per group
-// (bf16), codes
-constexpr int kXF16 = 0, kXBF16 = 1, kXE4M3 = 2, kXE4M3Block = 3, kXNvfp4 = 4;
-__host__ __device__ constexpr bool group_scaled(int xf) { return xf == kXBF16 || xf == kXE4M3Block; }
+enum XForm { kX16, kXScaled16, kXE4M3, kXE4M3Block, kXNvfp4 };
 
 struct Args {
   const void* x;
@@ -45,18 +44,16 @@ struct Args {
   const uint16_t* bias;
   uint16_t* y;
   int M, N, K;
-  int m0, rows;      // rows of x of this launch: m0 .. m0 + rows - 1
-  int groups;        // ceil(K / 128)
-  int seg_items;     // items of x in shared memory at a time
-  int kw;            // warps that share a weight tile (a power of two)
-  int units;         // sets of kWarps / kw weight tiles
+  int m0, rows;    // rows of x of this launch: m0 .. m0 + rows - 1
+  int groups;      // ceil(K / 128)
+  int seg_groups;  // groups of x in shared memory at a time
+  int kw, kw_log2; // warps that share a weight tile (a power of two)
+  int tiles;       // weight tiles of 16 rows
   int swizzled;
+  XForm form;
   int dt;
 };
 
-__device__ __forceinline__ int64_t sf_at(const Args& a, int64_t row, int col) {
-  return a.swizzled ? sf_offset_swizzled(row, col, a.K >> 4) : row * (a.K >> 4) + col;
-}
 __device__ __forceinline__ int64_t sf_bytes(const Args& a, int64_t n_rows) {
   const int cols = a.K >> 4;
   return a.swizzled ? ((n_rows + 127) >> 7) * (int64_t)((cols + 3) >> 2) * 512 : n_rows * cols;
@@ -67,54 +64,65 @@ struct WFrag {
   uint32_t c[2][4];
   uint32_t sf[2];
 };
-// A lane's loads of an item (kItem groups): the item's start in rows g and g +
-// 8, and where its 32 codes of each group lie from there.  Every load is made:
-// rows behind the last are row N - 1 again, their sums are dropped; codes
-// behind K are the last ones again, x is zero there.
+// A lane's rows g and g + 8 of a weight tile.  Rows behind the last are row N -
+// 1 again, their sums are dropped; codes behind K are the last ones again, x is
+// zero there.
 // LAY: 0 any K, 1 K % 32 == 0 with row-major factors, 2 with swizzled ones;
 // K % 32 == 0 has 16-byte loads of codes and 2-byte loads of factors.
 template <int LAY>
-struct WLoader {
+struct WRows {
   const uint8_t* c[2];
-  int row[2];
-  int col[kItem];  // first of the two 16-blocks, from the start of the row
+  const uint8_t* sf[2];
 
-  __device__ __forceinline__ void set_rows(const Args& a, int row0, int g) {
+  __device__ __forceinline__ void set(const Args& a, int row0, int g) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      row[h] = min(row0 + g + 8 * h, a.N - 1);
-      c[h] = a.w_codes + (int64_t)row[h] * (a.K >> 1);
+      const int row = min(row0 + g + 8 * h, a.N - 1);
+      c[h] = a.w_codes + (int64_t)row * (a.K >> 1);
+      sf[h] = a.w_sf + (LAY == 2 || (LAY == 0 && a.swizzled) ? sf_offset_swizzled(row, 0, a.K >> 4)
+                                                              : (int64_t)row * (a.K >> 4));
     }
   }
-  __device__ __forceinline__ void set_item(const Args& a, int item, int t) {
-    const int last = (a.K >> 4) - (LAY == 0 ? 1 : 2);
-#pragma unroll
-    for (int u = 0; u < kItem; ++u) col[u] = min((item * kItem + u) * (kGroup / 16) + 2 * t, last);
+  __device__ __forceinline__ int sf_at(const Args& a, int col) const {
+    return LAY == 2 || (LAY == 0 && a.swizzled) ? (col >> 2) * 512 + (col & 3) : col;
   }
-  __device__ __forceinline__ void load(const Args& a, int u, WFrag& f) const {
+  // Group `base` + u; whole: the sets' four groups lie inside K.
+  __device__ __forceinline__ void load(const Args& a, int base, int u, bool whole, int t, WFrag& f) const {
     const int64_t bytes = (int64_t)a.N * (a.K >> 1), n_sf = sf_bytes(a, a.N);
+    if (LAY == 0) {
+      const int last = (a.K >> 4) - 1;
+      const int c0 = min((base + u) * (kGroup / 16) + 2 * t, last), c1 = min(c0 + 1, last);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* p = c[h] + 8 * col[u];
-      f.sf[h] = 0;
-      if (LAY == 0) {
-        const int next = min(col[u] + 1, (a.K >> 4) - 1);
-        const uint8_t* p1 = c[h] + 8 * next;
-        const int64_t s0 = sf_at(a, row[h], col[u]), s1 = sf_at(a, row[h], next);
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t *p0 = c[h] + 8 * c0, *p1 = c[h] + 8 * c1;
+        const uint8_t *s0 = sf[h] + sf_at(a, c0), *s1 = sf[h] + sf_at(a, c1);
         uint2 v = make_uint2(0, 0), w = v;
-        if (FRT_SPAN_OK(p - a.w_codes, 8, bytes)) v = ld_stream(reinterpret_cast<const uint2*>(p));
+        if (FRT_SPAN_OK(p0 - a.w_codes, 8, bytes)) v = ld_stream(reinterpret_cast<const uint2*>(p0));
         if (FRT_SPAN_OK(p1 - a.w_codes, 8, bytes)) w = ld_stream(reinterpret_cast<const uint2*>(p1));
-        if (FRT_IDX_OK(s0, n_sf) && FRT_IDX_OK(s1, n_sf)) f.sf[h] = __ldg(a.w_sf + s0) | __ldg(a.w_sf + s1) << 8;
+        f.sf[h] = 0;
+        if (FRT_IDX_OK(s0 - a.w_sf, n_sf) && FRT_IDX_OK(s1 - a.w_sf, n_sf)) f.sf[h] = __ldg(s0) | __ldg(s1) << 8;
         f.c[h][0] = v.x;
         f.c[h][1] = v.y;
         f.c[h][2] = w.x;
         f.c[h][3] = w.y;
-      } else {
-        const int64_t s = LAY == 2 ? sf_offset_swizzled(row[h], col[u], a.K >> 4)
-                                   : (int64_t)row[h] * (a.K >> 4) + col[u];
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t *p, *s;
+        if (whole) {
+          const int col = base * (kGroup / 16) + 2 * t;
+          p = c[h] + 8 * col + u * (kGroup / 2);
+          s = sf[h] + sf_at(a, col) + u * (LAY == 2 ? 1024 : 8);
+        } else {
+          const int col = min((base + u) * (kGroup / 16) + 2 * t, (a.K >> 4) - 2);
+          p = c[h] + 8 * col;
+          s = sf[h] + sf_at(a, col);
+        }
         uint4 v = make_uint4(0, 0, 0, 0);
         if (FRT_SPAN_OK(p - a.w_codes, 16, bytes)) v = ld_stream(reinterpret_cast<const uint4*>(p));
-        if (FRT_SPAN_OK(s, 2, n_sf)) f.sf[h] = __ldg(reinterpret_cast<const uint16_t*>(a.w_sf + s));
+        f.sf[h] = 0;
+        if (FRT_SPAN_OK(s - a.w_sf, 2, n_sf)) f.sf[h] = __ldg(reinterpret_cast<const uint16_t*>(s));
         f.c[h][0] = v.x;
         f.c[h][1] = v.y;
         f.c[h][2] = v.z;
@@ -124,122 +132,171 @@ struct WLoader {
   }
 };
 
-// Four elements of row r (0 based within the launch) at column k as two
-// binary16 pairs, and the factor of (row, group): a warp holds the 128 elements
-// of a group.
-template <int XF>
-__device__ __forceinline__ uint2 load_x4(const Args& a, int r, int k, float* scale) {
+// Eight elements of row r (within the launch) from column k on: the raw bits,
+// and for NVFP4 their factor.
+struct XRaw {
+  uint4 v;
+  uint32_t sf;
+};
+__device__ __forceinline__ XRaw load_x(const Args& a, int r, int k) {
+  XRaw o;
+  o.v = make_uint4(0, 0, 0, 0);
+  o.sf = 0;
+  if (r >= a.rows || k >= a.K) return o;
   const int64_t row = a.m0 + r;
-  const bool on = r < a.rows && k < a.K;
-  const int64_t at = row * a.K + k;
-  const int64_t n = (int64_t)a.M * a.K;
-  uint2 o = make_uint2(0, 0);
-  *scale = 1.0f;
-  if (XF == kXF16 || XF == kXBF16) {
-    if (on && FRT_SPAN_OK(at, 4, n)) o = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + at);
-    if (XF == kXBF16) {
-      float2 u = Pack16<FRT_BF16>::to_float2(o.x), v = Pack16<FRT_BF16>::to_float2(o.y);
-      const float s = pow2_to_half_range(warp_max_abs(absmax4(u.x, u.y, v.x, v.y)));
-      o.x = Pack16<FRT_F16>::from_float2(u.x * s, u.y * s);
-      o.y = Pack16<FRT_F16>::from_float2(v.x * s, v.y * s);
-      *scale = 1.0f / s;
-    }
-  } else if (XF == kXE4M3 || XF == kXE4M3Block) {
-    uint32_t w = 0;
-    if (on && FRT_SPAN_OK(at, 4, n)) w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.x) + at);
-    e4m3x4_to_half2(w, &o.x);
-    const int64_t sa = row * a.groups + k / kGroup;
-    if (XF == kXE4M3Block && on && FRT_IDX_OK(sa, (int64_t)a.M * a.groups)) *scale = a.x_scales[sa];
+  const int64_t at = row * a.K + k, n = (int64_t)a.M * a.K;
+  if (!FRT_SPAN_OK(at, 8, n)) return o;
+  const uint8_t* x = static_cast<const uint8_t*>(a.x);
+  if (a.form == kX16 || a.form == kXScaled16) {
+    o.v = ld_plain(reinterpret_cast<const uint4*>(x + 2 * at));
+  } else if (a.form != kXNvfp4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(x + at);
+    o.v.x = u.x;
+    o.v.y = u.y;
   } else {
-    uint32_t w = 0, s = 0;
-    if (on && FRT_SPAN_OK(at >> 1, 2, n >> 1))
-      w = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(a.x) + (at >> 1));
-    if (on) {
-      const int64_t sa = sf_at(a, row, k >> 4);
-      if (FRT_IDX_OK(sa, sf_bytes(a, a.M))) s = a.x_sf[sa];
-    }
-    uint32_t h[4], f[2];
-    e2m1x8_to_half2(w, h);
-    e4m3x4_to_half2(s * 0x0101u, f);
-    o = make_uint2(hmul2(h[0], f[0]), hmul2(h[1], f[0]));
+    o.v.x = *reinterpret_cast<const uint32_t*>(x + (at >> 1));
+    const int64_t sa = a.swizzled ? sf_offset_swizzled(row, k >> 4, a.K >> 4) : row * (a.K >> 4) + (k >> 4);
+    if (FRT_IDX_OK(sa, sf_bytes(a, a.M))) o.sf = a.x_sf[sa];
+  }
+  return o;
+}
+// The same as binary16; 16 lanes hold a group of a row, *scale is its factor.
+__device__ __forceinline__ uint4 convert_x(const Args& a, const XRaw& raw, int r, int group, float* scale) {
+  *scale = 1.0f;
+  uint4 o = raw.v;
+  if (a.form == kXScaled16) {
+    float2 v[4];
+    unpack_pairs<FRT_BF16, 4>(&o.x, v);
+    const float amax = fmaxf(absmax4(v[0].x, v[0].y, v[1].x, v[1].y), absmax4(v[2].x, v[2].y, v[3].x, v[3].y));
+    const float s = pow2_to_half_range(half_warp_max_abs(amax));
+    mul_pairs<4>(v, s);
+    pack_pairs<FRT_F16, 4>(v, &o.x);
+    *scale = 1.0f / s;
+  } else if (a.form == kXE4M3 || a.form == kXE4M3Block) {
+    const uint2 u = make_uint2(raw.v.x, raw.v.y);
+    e4m3x4_to_half2(u.x, &o.x);
+    e4m3x4_to_half2(u.y, &o.z);
+    const int64_t at = (int64_t)(a.m0 + r) * a.groups + group;
+    if (a.form == kXE4M3Block && r < a.rows && FRT_IDX_OK(at, (int64_t)a.M * a.groups)) *scale = a.x_scales[at];
+  } else if (a.form == kXNvfp4) {
+    uint32_t f[2];
+    e2m1x8_to_half2(raw.v.x, &o.x);
+    e4m3x4_to_half2(raw.sf * 0x0101u, f);
+    o = make_uint4(hmul2(o.x, f[0]), hmul2(o.y, f[0]), hmul2(o.z, f[0]), hmul2(o.w, f[0]));
   }
   return o;
 }
 
-template <int NT, int XF, int LAY>
+template <int DT>
+__device__ __forceinline__ float value16(uint16_t w) {
+  return Pack16<DT>::to_float2((uint32_t)w).x;
+}
+
+constexpr int kRedStride = 20;  // floats between two rows of x of a warp's sums
+
+// Floats of a warp's sums of a tile, [row of x][weight row].
+__host__ __device__ constexpr int sum_floats(int nt, int mr) { return (nt == 1 ? mr : 8 * nt) * kRedStride; }
+
+// SCALED: x has a factor per row and group.
+template <int NT, bool SCALED, int LAY>
 __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int mr = NT == 1 ? min(a.rows, 8) : 8;  // rows of x that shared memory holds per 8
-  const int step_words = NT * mr * 4;           // 16-byte words of 32 k
-  constexpr int kRed = NT * 8 * 17;             // a warp's sums, [row of x][weight row]
-  float* red = reinterpret_cast<float*>(smem);
-  uint2* xf = reinterpret_cast<uint2*>(smem + sizeof(float) * kWarps * kRed);
-  float* xs = reinterpret_cast<float*>(xf + (size_t)a.seg_items * kItem * 8 * step_words);
-
-  const int kw = a.kw, ks = warp & (kw - 1), rw = warp / kw, tiles_at_once = kWarps / kw;
-  const int items = (a.groups + kItem - 1) / kItem;
-  const bool one_seg = a.seg_items >= items;
+  const int step = NT * mr * 4;                 // 16-byte words of 32 k
+  const int red_warp = sum_floats(NT, mr);
+  float* red = reinterpret_cast<float*>(smem);  // [2][warp][row of x][weight row]
+  uint4* xf = reinterpret_cast<uint4*>(smem + sizeof(float) * 2 * kWarps * red_warp);
+  float* xs = reinterpret_cast<float*>(xf + (size_t)a.seg_groups * 4 * step);
   // rows of x that are not there: the last one again, its sums are dropped
-  const uint4* x_lane = reinterpret_cast<const uint4*>(xf) + min(g, mr - 1) * 4 + t;
+  const uint4* x_lane = xf + min(g, mr - 1) * 4 + t;
 
-  // This warp's items: of each unit the items ks, ks + kw, ... of its weight
-  // tile, unit after unit.
+  const int kw = a.kw, ks = warp & (kw - 1), rw = warp >> a.kw_log2, at_once = kWarps >> a.kw_log2;
+  // the tile of this warp in a round (tiles are dealt to the CTAs in turn)
+  auto tile_of = [&](int round) { return (round * at_once + rw) * (int)gridDim.x + (int)blockIdx.x; };
+  const int per_round = at_once * (int)gridDim.x;
+  const int rounds = a.tiles / per_round + (a.tiles % per_round > (int)blockIdx.x);  // of this CTA's first warp
+
+  // This warp's groups: of each tile and segment of k a contiguous share, in
+  // sets of kAhead.  end == 0: no more.
   struct Cursor {
-    int unit, item;
+    int round, seg, base, end;
+  };
+  auto share = [&](Cursor& c) {
+    const int len = min(a.seg_groups, a.groups - c.seg);
+    c.base = c.seg + (len * ks >> a.kw_log2);
+    c.end = c.seg + (len * (ks + 1) >> a.kw_log2);
+    if (tile_of(c.round) >= a.tiles) c.end = 0;
   };
   auto advance = [&](Cursor c) {
-    c.item += kw;
-    if (c.item >= items) {
-      c.item = ks;
-      c.unit += gridDim.x;
+    c.base += kAhead;
+    while (c.base >= c.end && c.end > 0) {
+      c.seg += a.seg_groups;
+      if (c.seg >= a.groups) {
+        c.seg = 0;
+        ++c.round;
+      }
+      share(c);
     }
     return c;
   };
-  WFrag w[kItem];
-  WLoader<LAY> loader;
-  Cursor cur = {(int)blockIdx.x, ks};  // (kw <= items)
-  loader.set_rows(a, (cur.unit * tiles_at_once + rw) * 16, g);
-  loader.set_item(a, ks, t);
+  auto is_whole = [&](const Cursor& c) { return LAY != 0 && (c.base + kAhead) * kGroup <= a.K; };
+  WFrag w[kAhead];
+  WRows<LAY> rows;
+  Cursor cur = {0, 0, 0, 0};
+  share(cur);
+  rows.set(a, tile_of(0) * 16, g);
 #pragma unroll
-  for (int u = 0; u < kItem; ++u) loader.load(a, u, w[u]);  // constant inputs: before the wait
+  for (int u = 0; u < kAhead; ++u)
+    if (cur.base + u < cur.end) rows.load(a, cur.base, u, is_whole(cur), t, w[u]);  // constant inputs: before the wait
   const float w_scale = __ldg(a.w_scale);
   pdl_enter();
-  const float scale = w_scale * (XF == kXE4M3 || XF == kXNvfp4 ? a.x_scales[0] : 1.0f);
+  const float scale = w_scale * (a.form == kXE4M3 || a.form == kXNvfp4 ? a.x_scales[0] : 1.0f);
 
-  for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+  for (int round = 0; round < rounds; ++round) {
     float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-    for (int seg = 0; seg < items; seg += a.seg_items) {
-      const int seg_end = min(seg + a.seg_items, items);
-      if (!one_seg || unit == (int)blockIdx.x) {
-        if (!one_seg) __syncthreads();  // the last segment is read
-        const int rows = NT == 1 ? mr : 8 * NT;
-        const int n_groups = min(seg_end * kItem, a.groups) - seg * kItem;
-        for (int i = warp; i < rows * n_groups; i += kWarps) {
-          const int r = i % rows, c = i / rows;
-          float s;
-          const uint2 v = load_x4<XF>(a, r, (seg * kItem + c) * kGroup + 4 * lane, &s);
-          // steps 2p and 2p + 1 of a lane side by side
-          const int pair = (lane & 7) >> 1;
-          xf[((c * 4 + pair) * step_words + ((r >> 3) * mr + (r & 7)) * 4 + (lane >> 3)) * 2 + (lane & 1)] = v;
-          if (group_scaled(XF) && lane == 0) xs[c * (8 * NT) + r] = s;
+    for (int seg = 0; seg < a.groups; seg += a.seg_groups) {
+      if (a.seg_groups < a.groups || round == 0) {
+        if (seg > 0 || round > 0) __syncthreads();  // the last segment is read
+        const int n_rows = NT == 1 ? mr : 8 * NT;
+        const int n = n_rows * min(a.seg_groups, a.groups - seg);  // (row, group) pairs, one to 16 lanes
+        constexpr int kBatch = 4;
+        for (int i0 = warp * 2; i0 < n; i0 += 2 * kWarps * kBatch) {
+          XRaw raw[kBatch];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * 2 * kWarps + (lane >> 4);
+            const int c = i / n_rows, r = i - c * n_rows;
+            raw[b] = load_x(a, i < n ? r : a.rows, (seg + c) * kGroup + 8 * (lane & 15));
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * 2 * kWarps + (lane >> 4);
+            const int c = i / n_rows, r = i - c * n_rows;
+            float s;
+            const uint4 v = convert_x(a, raw[b], i < n ? r : a.rows, seg + c, &s);
+            if (i < n) {
+              xf[(c * 4 + (lane & 3)) * step + ((r >> 3) * mr + (r & 7)) * 4 + ((lane & 15) >> 2)] = v;
+              if (SCALED && (lane & 15) == 0) xs[c * (8 * NT) + r] = s;
+            }
+          }
         }
         __syncthreads();
       }
-      while (cur.unit == unit && cur.item < seg_end) {
+      while (cur.end > 0 && cur.round == round && cur.seg == seg) {
         const Cursor next = advance(cur);
-        if (next.unit != unit) loader.set_rows(a, (next.unit * tiles_at_once + rw) * 16, g);
-        loader.set_item(a, next.item, t);
+        if (next.round != round && next.end > 0) rows.set(a, tile_of(next.round) * 16, g);
+        const bool next_whole = is_whole(next);
+        const uint4* xb = x_lane + (cur.base - seg) * 4 * step;
+        const float* xsb = xs + (cur.base - seg) * 8 * NT + 2 * t;
 #pragma unroll
-        for (int u = 0; u < kItem; ++u) {
-          const int group = cur.item * kItem + u;
-          if (group < a.groups) {
-            const int c = group - seg * kItem;
+        for (int u = 0; u < kAhead; ++u) {
+          if (cur.base + u < cur.end) {
             float part[NT][4];
-            if (group_scaled(XF)) {
+            if (SCALED) {
 #pragma unroll
               for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.0f;
             }
@@ -257,97 +314,167 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
                 h1[e] = hmul2(h1[e], sc[2 + (q >> 1)]);
               }
               const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
-              const uint4* xb = x_lane + (c * 4 + q) * step_words;
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 const uint4 bv = xb[n * 32];
-                mma_16816(group_scaled(XF) ? part[n] : acc[n], a0, bv.x, bv.y);
-                mma_16816(group_scaled(XF) ? part[n] : acc[n], a1, bv.z, bv.w);
+                mma_16816(SCALED ? part[n] : acc[n], a0, bv.x, bv.y);
+                mma_16816(SCALED ? part[n] : acc[n], a1, bv.z, bv.w);
+              }
+              xb += step;
+            }
+            if (SCALED) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const float2 s = *reinterpret_cast<const float2*>(xsb + u * 8 * NT + 8 * n);
+                acc[n][0] = fmaf(part[n][0], s.x, acc[n][0]);
+                acc[n][1] = fmaf(part[n][1], s.y, acc[n][1]);
+                acc[n][2] = fmaf(part[n][2], s.x, acc[n][2]);
+                acc[n][3] = fmaf(part[n][3], s.y, acc[n][3]);
               }
             }
-            if (group_scaled(XF)) {
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float s = xs[c * (8 * NT) + 8 * n + 2 * t + e];
-                  acc[n][e] = fmaf(part[n][e], s, acc[n][e]);
-                  acc[n][2 + e] = fmaf(part[n][2 + e], s, acc[n][2 + e]);
-                }
-            }
           }
-          loader.load(a, u, w[u]);
+          if (next.base + u < next.end) rows.load(a, next.base, u, next_whole, t, w[u]);
         }
         cur = next;
       }
     }
-    // sums of the warps that share a weight tile
-    float* mine = red + warp * kRed;
+    // The sums through shared memory: of the warp's own tile, or of the kw warps
+    // that share one.  Two sets of them, so that one barrier a round is enough.
+    float* sums = red + (size_t)(round & 1) * kWarps * red_warp;
+    float* mine = sums + warp * red_warp + g;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mine[(8 * n + 2 * t + e) * 17 + g] = acc[n][e];
-        mine[(8 * n + 2 * t + e) * 17 + g + 8] = acc[n][2 + e];
+        const int r = 8 * n + 2 * t + e;
+        if (NT > 1 || r < mr) {
+          mine[r * kRedStride] = acc[n][e];
+          mine[r * kRedStride + 8] = acc[n][2 + e];
+        }
       }
-    __syncthreads();
-    for (int i = threadIdx.x; i < tiles_at_once * 16 * a.rows; i += kThreads) {
-      const int col = i & 15, tile = (i >> 4) % tiles_at_once, r = (i >> 4) / tiles_at_once;
-      const int n = (unit * tiles_at_once + tile) * 16 + col;
-      if (n >= a.N) continue;
-      float sum = 0.0f;
-      for (int k = 0; k < kw; ++k) sum += red[(tile * kw + k) * kRed + r * 17 + col];
-      sum *= scale;
-      const bool half = a.dt == FRT_F16;
-      if (a.bias != nullptr && FRT_IDX_OK(n, a.N)) {
-        const uint32_t bw = a.bias[n];
-        sum += half ? Pack16<FRT_F16>::to_float2(bw).x : Pack16<FRT_BF16>::to_float2(bw).x;
+    if (kw == 1)
+      __syncwarp();
+    else
+      __syncthreads();
+    const int first = kw == 1 ? lane : threadIdx.x, threads = kw == 1 ? 32 : kThreads;
+    const int my_tiles = kw == 1 ? 1 : at_once;
+    const bool half = a.dt == FRT_F16;
+    if (NT == 1) {  // one output to a thread, neighbours along n
+      for (int i = first; i < my_tiles * 16 * a.rows; i += threads) {
+        const int col = i & 15, j = (i >> 4) & (my_tiles - 1), r = (i >> 4) / my_tiles;
+        const int q = kw == 1 ? rw : j;
+        const int n = ((round * at_once + q) * (int)gridDim.x + (int)blockIdx.x) * 16 + col;
+        if (n >= a.N) continue;
+        const float* p = sums + (q << a.kw_log2) * red_warp + r * kRedStride + col;
+        float sum = 0.0f;
+        for (int k = 0; k < kw; ++k) sum += p[k * red_warp];
+        sum *= scale;
+        if (a.bias != nullptr && FRT_IDX_OK(n, a.N))
+          sum += half ? value16<FRT_F16>(a.bias[n]) : value16<FRT_BF16>(a.bias[n]);
+        const int64_t at = (int64_t)(a.m0 + r) * a.N + n;
+        if (FRT_IDX_OK(at, (int64_t)a.M * a.N))
+          a.y[at] = (uint16_t)(half ? Pack16<FRT_F16>::from_float2(sum, 0.0f) : Pack16<FRT_BF16>::from_float2(sum, 0.0f));
       }
-      const int64_t at = (int64_t)(a.m0 + r) * a.N + n;
-      if (FRT_IDX_OK(at, (int64_t)a.M * a.N))
-        a.y[at] = (uint16_t)(half ? Pack16<FRT_F16>::from_float2(sum, 0.0f)
-                                  : Pack16<FRT_BF16>::from_float2(sum, 0.0f));
+      continue;
     }
-    __syncthreads();
+    const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+    for (int i = first; i < my_tiles * 2 * a.rows; i += threads) {
+      const int o = i & 1, j = (i >> 1) & (my_tiles - 1), r = (i >> 1) / my_tiles;
+      const int q = kw == 1 ? rw : j;
+      const int n = ((round * at_once + q) * (int)gridDim.x + (int)blockIdx.x) * 16 + 8 * o;
+      if (n >= a.N) continue;
+      float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k = 0; k < kw; ++k) {
+        const float* p = sums + ((q << a.kw_log2) + k) * red_warp + r * kRedStride + 8 * o;
+        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+        sum[0] += u.x;
+        sum[1] += u.y;
+        sum[2] += u.z;
+        sum[3] += u.w;
+        sum[4] += v.x;
+        sum[5] += v.y;
+        sum[6] += v.z;
+        sum[7] += v.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum[e] *= scale;
+        if (a.bias != nullptr && n + e < a.N && FRT_IDX_OK(n + e, a.N)) {
+          const uint16_t b = a.bias[n + e];
+          sum[e] += half ? value16<FRT_F16>(b) : value16<FRT_BF16>(b);
+        }
+      }
+      uint32_t out[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        out[e] = half ? Pack16<FRT_F16>::from_float2(sum[2 * e], sum[2 * e + 1])
+                      : Pack16<FRT_BF16>::from_float2(sum[2 * e], sum[2 * e + 1]);
+      const int64_t at = (int64_t)(a.m0 + r) * a.N + n;
+      if (wide) {
+        if (FRT_SPAN_OK(at, 8, (int64_t)a.M * a.N))
+          *reinterpret_cast<uint4*>(a.y + at) = make_uint4(out[0], out[1], out[2], out[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < a.N && FRT_IDX_OK(at + e, (int64_t)a.M * a.N))
+            a.y[at + e] = (uint16_t)(out[e >> 1] >> (16 * (e & 1)));
+      }
+    }
   }
 }
 
-template <int NT, int XF, int LAY>
+template <int NT, bool SCALED, int LAY>
 frt_status launch_one(Args a, cudaStream_t stream) {
-  const int items = (a.groups + kItem - 1) / kItem;
-  a.kw = 1;
-  while (a.kw < kWarps && a.kw * 2 <= items) a.kw *= 2;
-  const int tiles = (a.N + 15) / 16, at_once = kWarps / a.kw;
-  a.units = (tiles + at_once - 1) / at_once;
-  const size_t mr = NT == 1 && a.rows < 8 ? a.rows : 8;
-  const size_t item_bytes = (size_t)kItem * (8 * NT * mr * 4 * 8 + (group_scaled(XF) ? 8 * NT * 4 : 0));
-  const size_t red = sizeof(float) * kWarps * NT * 8 * 17;
-  int64_t seg = kXBytes / item_bytes;
-  if (seg < 1) seg = 1;
-  if (seg > a.kw) seg -= seg % a.kw;
-  a.seg_items = (int)(seg < items ? seg : items);
-  const size_t smem = red + a.seg_items * item_bytes;
+  constexpr int kPerSM = NT <= 2 ? 2 : 1;
+  a.tiles = (int)(((int64_t)a.N + 15) / 16);
+  const int mr = NT == 1 && a.rows < 8 ? a.rows : 8;
+  const size_t group_bytes = (size_t)4 * NT * mr * 4 * 16 + (SCALED ? 8 * NT * 4 : 0);
+  const size_t red = sizeof(float) * 2 * kWarps * sum_floats(NT, mr);
+  // all of x in shared memory where it fits, with the CTAs that share an SM
+  // where that fits
+  const size_t all = red + a.groups * group_bytes;
+  const int per_sm = all <= 112 * 1024 ? kPerSM : 1;
+  const int fit = (int)std::min<size_t>((225 * 1024 - red) / group_bytes, a.groups);
+  // warps to a tile: the fewest rounds, a round being its share of k and the
+  // cost of a round itself (about a group and a half)
+  int64_t best = 0;
+  for (int kw = 1, log2 = 0; kw <= kWarps && kw <= a.groups; kw *= 2, ++log2) {
+    const int64_t slots = (int64_t)kSMs * per_sm * (kWarps / kw);
+    const int64_t rounds = (a.tiles + slots - 1) / slots;
+    const int64_t cost = rounds * (2 * ((a.groups + kw - 1) / kw) + 3);
+    if (kw == 1 || cost < best) {
+      best = cost;
+      a.kw = kw;
+      a.kw_log2 = log2;
+    }
+  }
+  while (fit < a.groups && a.kw * kAhead > fit) {  // a segment is whole sets for every warp
+    a.kw /= 2;
+    --a.kw_log2;
+  }
+  a.seg_groups = fit >= a.groups ? a.groups : fit / (a.kw * kAhead) * (a.kw * kAhead);
+  const size_t smem = red + a.seg_groups * group_bytes;
   static std::atomic<int> opted{48 * 1024};
-  const frt_status st = opt_in_smem(matvec_kernel<NT, XF, LAY>, smem, opted);
+  const frt_status st = opt_in_smem(matvec_kernel<NT, SCALED, LAY>, smem, opted);
   if (st != FRT_OK) return st;
-  const int resident = kSMs * (NT <= 2 ? 2 : 1);
-  const unsigned grid = (unsigned)(a.units < resident ? a.units : resident);
-  return launch(matvec_kernel<NT, XF, LAY>, dim3(grid), dim3(kThreads), smem, stream, a);
+  const int ctas = kSMs * per_sm;
+  const unsigned grid = (unsigned)(a.tiles < ctas ? a.tiles : ctas);
+  return launch(matvec_kernel<NT, SCALED, LAY>, dim3(grid), dim3(kThreads), smem, stream, a);
 }
-template <int NT, int XF>
-frt_status launch_wide(const Args& a, cudaStream_t stream) {
-  if (a.K % 32 != 0) return launch_one<NT, XF, 0>(a, stream);
-  return a.swizzled ? launch_one<NT, XF, 2>(a, stream) : launch_one<NT, XF, 1>(a, stream);
+template <int NT, bool SCALED>
+frt_status launch_layout(const Args& a, cudaStream_t stream) {
+  if (a.K % 32 != 0) return launch_one<NT, SCALED, 0>(a, stream);
+  return a.swizzled ? launch_one<NT, SCALED, 2>(a, stream) : launch_one<NT, SCALED, 1>(a, stream);
 }
-template <int XF>
+template <bool SCALED>
 frt_status launch_rows(Args a, cudaStream_t stream) {
   for (a.m0 = 0; a.m0 < a.M; a.m0 += 64) {
     a.rows = a.M - a.m0 < 64 ? a.M - a.m0 : 64;
-    const frt_status st = a.rows <= 8    ? launch_wide<1, XF>(a, stream)
-                          : a.rows <= 16 ? launch_wide<2, XF>(a, stream)
-                          : a.rows <= 32 ? launch_wide<4, XF>(a, stream)
-                          : a.rows <= 48 ? launch_wide<6, XF>(a, stream)
-                                         : launch_wide<8, XF>(a, stream);
+    const frt_status st = a.rows <= 8    ? launch_layout<1, SCALED>(a, stream)
+                          : a.rows <= 16 ? launch_layout<2, SCALED>(a, stream)
+                          : a.rows <= 32 ? launch_layout<4, SCALED>(a, stream)
+                          : a.rows <= 48 ? launch_layout<6, SCALED>(a, stream)
+                                         : launch_layout<8, SCALED>(a, stream);
     if (st != FRT_OK) return st;
   }
   return FRT_OK;
@@ -388,9 +515,10 @@ extern "C" frt_status frt_matvec_nvfp4(const void* x, const float* x_scales, con
   a.swizzled = sf_layout == FRT_SF_SWIZZLED_128X4;
   a.dt = dt;
   switch (x_format) {
-    case FRT_X_16BIT: return dt == FRT_F16 ? launch_rows<kXF16>(a, stream) : launch_rows<kXBF16>(a, stream);
-    case FRT_X_E4M3: return launch_rows<kXE4M3>(a, stream);
-    case FRT_X_E4M3_BLOCK: return launch_rows<kXE4M3Block>(a, stream);
-    default: return launch_rows<kXNvfp4>(a, stream);
+    case FRT_X_16BIT: a.form = dt == FRT_F16 ? kX16 : kXScaled16; break;
+    case FRT_X_E4M3: a.form = kXE4M3; break;
+    case FRT_X_E4M3_BLOCK: a.form = kXE4M3Block; break;
+    default: a.form = kXNvfp4; break;
   }
+  return a.form == kXScaled16 || a.form == kXE4M3Block ? launch_rows<true>(a, stream) : launch_rows<false>(a, stream);
 }
