@@ -43,7 +43,9 @@ struct WriteArgs {
   int32_t* status;
   int M, Hq, Hkv, L;  // L = hd / 16: lanes of a head, and 16-byte chunks of half a head
   int max_pos, capacity;
-  float eps;
+  float eps, inv_hd;
+  double inv_hd64;
+  bool narrow;                // (token, head) indices fit 32 bits
   int64_t warps_q, warps_kv;  // warps that hold Q heads, and K (or V) heads
 };
 
@@ -78,7 +80,7 @@ __device__ __forceinline__ float amax8_or_inf(const float* y) {
 // P: lanes of a head, the next power of two from L (4, 8 or 16; 1 and 2 for
 // the smallest heads).
 template <int DT, int P>
-__global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) write_kernel(WriteArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int kind = w < a.warps_q ? kQ : w < a.warps_q + a.warps_kv ? kK : kV;
@@ -88,43 +90,46 @@ __global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a) {
   const int l = lane % P;
   const int heads = a.Hq + 2 * a.Hkv;
   bool on = l < a.L && item < (int64_t)a.M * H;
-  const int64_t i = on ? item / H : 0;
+  int64_t i = 0;
+  if (on) i = a.narrow ? (int64_t)((uint32_t)item / (uint32_t)H) : item / H;
   const int h = on ? (int)(item - i * H) : 0;
   const int C = 2 * a.L;  // chunks of a head
 
-  // constant inputs before the wait
+  // The loads that depend on nothing are issued together: positions (constant,
+  // before the wait) and qkv; the RoPE rows follow the position.
+  const bool there = on;
   int p = 0, slot = 0;
   if (on && FRT_IDX_OK(i, a.M)) {
     p = __ldg(a.positions + i);
     slot = a.slots != nullptr ? __ldg(a.slots + i) : p;
-    if (p < 0 || p >= a.max_pos || slot < 0 || slot >= a.capacity) {
-      if (a.status != nullptr && l == 0) atomicOr(a.status, 1);
-      on = false;
-    }
   }
   const uint4* norm_w = kind == kQ ? a.q_norm_w : a.k_norm_w;
   const bool normed = kind != kV && norm_w != nullptr;
   uint4 w_lo = make_uint4(0, 0, 0, 0), w_hi = w_lo;
-  float2 cs[4], sn[4], nsn[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) cs[e] = sn[e] = nsn[e] = make_float2(0.0f, 0.0f);
   if (on && normed && FRT_IDX_OK(l + a.L, C)) {
     w_lo = __ldg(norm_w + l);
     w_hi = __ldg(norm_w + l + a.L);
-  }
-  if (on && kind != kV && FRT_SPAN_OK((int64_t)p * C + 2 * l, 2, (int64_t)a.max_pos * C)) {
-    const float* c = reinterpret_cast<const float*>(a.cos_tab + (int64_t)p * C + 2 * l);
-    const float* s = reinterpret_cast<const float*>(a.sin_tab + (int64_t)p * C + 2 * l);
-    load_rope_pairs<4>(c, s, cs, sn, nsn);
   }
   const float gs = kind == kQ ? 1.0f : __ldg(a.kv_scales + (kind - kK));
   pdl_enter();
 
   const int64_t in0 = (i * heads + (kind == kQ ? h : kind == kK ? a.Hq + h : a.Hq + a.Hkv + h)) * C + l;
   uint4 x_lo = make_uint4(0, 0, 0, 0), x_hi = x_lo;
-  if (on && FRT_IDX_OK(in0 + a.L, (int64_t)a.M * heads * C)) {
+  if (there && FRT_IDX_OK(in0 + a.L, (int64_t)a.M * heads * C)) {
     x_lo = ld_stream(a.qkv + in0);
     x_hi = ld_stream(a.qkv + in0 + a.L);
+  }
+  if (on && (p < 0 || p >= a.max_pos || slot < 0 || slot >= a.capacity)) {
+    if (a.status != nullptr && l == 0) atomicOr(a.status, 1);
+    on = false;
+  }
+  float2 cs[4], sn[4], nsn[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) cs[e] = sn[e] = nsn[e] = make_float2(0.0f, 0.0f);
+  if (on && kind != kV && FRT_SPAN_OK((int64_t)p * C + 2 * l, 2, (int64_t)a.max_pos * C)) {
+    const float* c = reinterpret_cast<const float*>(a.cos_tab + (int64_t)p * C + 2 * l);
+    const float* s = reinterpret_cast<const float*>(a.sin_tab + (int64_t)p * C + 2 * l);
+    load_rope_pairs<4>(c, s, cs, sn, nsn);
   }
   float2 lo[4], hi[4];
   unpack_pairs<DT, 4>(&x_lo.x, lo);
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a) {
   if (kind == kQ) {
     if (normed) {
       const float ss = group_sum<P>(sum_squares_pairs<4>(lo, hi));
-      const float r = head_rstd(ss, 1.0f / (float)(16 * a.L), a.eps);
+      const float r = head_rstd(ss, a.inv_hd, a.eps);
       float2 wl[4], wh[4];
       unpack_pairs<DT, 4>(&w_lo.x, wl);
       unpack_pairs<DT, 4>(&w_hi.x, wh);
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a) {
               ((double)(hi[e].x * hi[e].x) + (double)(hi[e].y * hi[e].y));
 #pragma unroll
       for (int o = P / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      r = Split32(rsqrt_f64(ss / (double)(16 * a.L) + (double)a.eps));
+      r = Split32(rsqrt_f64(fma(ss, a.inv_hd64, (double)a.eps)));
       float2 wl[4], wh[4];
       unpack_pairs<DT, 4>(&w_lo.x, wl);
       unpack_pairs<DT, 4>(&w_hi.x, wh);
@@ -236,6 +241,9 @@ frt_status launch_write(const WriteArgs& a0, cudaStream_t stream) {
   WriteArgs a = a0;
   const int P = a.L > 8 ? 16 : a.L > 4 ? 8 : a.L > 2 ? 4 : a.L;
   const int per = 32 / P;
+  a.narrow = (int64_t)a.M * a.Hq < 0x7FFFFFFF;
+  a.inv_hd64 = 1.0 / (16 * a.L);
+  a.inv_hd = (float)a.inv_hd64;
   a.warps_q = ((int64_t)a.M * a.Hq + per - 1) / per;
   a.warps_kv = ((int64_t)a.M * a.Hkv + per - 1) / per;
   const int64_t blocks = (a.warps_q + 2 * a.warps_kv + kWarps - 1) / kWarps;
@@ -250,43 +258,65 @@ frt_status launch_write(const WriteArgs& a0, cudaStream_t stream) {
   }
 }
 
-// Reader: a thread takes 8 codes (4 bytes) of one tensor to one 16-byte store;
-// bound by the 4 B an element pair it writes.
+// Reader: bound by the 4 B an element pair it writes.  A thread takes kReadUnits
+// units of 8 codes (4 bytes to one 16-byte store) of K and of V, their loads
+// issued together.
+constexpr int kReadUnits = 2;
 template <int DT>
 __global__ void __launch_bounds__(kThreads) read_kernel(const uint32_t* k_codes, const uint8_t* k_sf,
                                                         const uint32_t* v_codes, const uint8_t* v_sf,
                                                         const float* kv_scales, const int32_t* slots, uint4* k_out,
                                                         uint4* v_out, int32_t* status, int n, int Hkv, int L,
                                                         int capacity) {
-  const int t = blockIdx.y;
-  const float gs = __ldg(kv_scales + t);
+  const float gs[2] = {__ldg(kv_scales), __ldg(kv_scales + 1)};
   pdl_enter();
   const int U = 2 * L * Hkv;  // 8-element units of a slot
-  const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t i = at / U;
-  const int u = (int)(at - i * U);
-  if (i >= n || !FRT_IDX_OK(i, n)) return;
-  const int slot = slots != nullptr ? __ldg(slots + i) : (int)i;
-  if (slot < 0 || slot >= capacity) {
-    if (status != nullptr && u == 0) atomicOr(status, 1);
-    return;
-  }
-  const uint32_t* codes = t == 0 ? k_codes : v_codes;
-  const uint8_t* sf = t == 0 ? k_sf : v_sf;
-  const int64_t c = (int64_t)slot * U + u;
-  const int64_t s = ((int64_t)(slot >> 2) * (U >> 1) + (u >> 1)) * 4 + (slot & 3);
-  if (!FRT_IDX_OK(c, (int64_t)capacity * U) || !FRT_IDX_OK(s, (int64_t)((capacity + 3) >> 2) * (U >> 1) * 4)) return;
-  const uint32_t w = __ldg(codes + c);
-  const float f = e4m3_value(__ldg(sf + s));
-  uint32_t o[4];
+  const int64_t at0 = (int64_t)blockIdx.x * (kThreads * kReadUnits) + threadIdx.x;
+  const int64_t total = (int64_t)n * U;
+  int slot[kReadUnits], u[kReadUnits];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * e)), __NV_E2M1);
-    const float2 v = __half22float2(__half2(h));
-    o[e] = Pack16<DT>::from_float2((v.x * f) * gs, (v.y * f) * gs);
+  for (int j = 0; j < kReadUnits; ++j) {
+    const int64_t at = at0 + j * kThreads;
+    const int64_t i = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)at / (uint32_t)U) : at / U;
+    u[j] = (int)(at - i * U);
+    slot[j] = -1;
+    if (at < total && FRT_IDX_OK(i, n)) {
+      slot[j] = slots != nullptr ? __ldg(slots + i) : (int)i;
+      if (slot[j] < 0 || slot[j] >= capacity) {
+        if (status != nullptr && u[j] == 0) atomicOr(status, 1);
+        slot[j] = -1;
+      }
+    }
   }
-  const int64_t out = i * U + u;
-  if (FRT_IDX_OK(out, (int64_t)n * U)) (t == 0 ? k_out : v_out)[out] = make_uint4(o[0], o[1], o[2], o[3]);
+  uint32_t w[kReadUnits][2], f[kReadUnits][2];
+#pragma unroll
+  for (int j = 0; j < kReadUnits; ++j) {
+    const int64_t c = (int64_t)slot[j] * U + u[j];
+    const int64_t s = ((int64_t)(slot[j] >> 2) * (U >> 1) + (u[j] >> 1)) * 4 + (slot[j] & 3);
+    const bool on = slot[j] >= 0 && FRT_IDX_OK(c, (int64_t)capacity * U) &&
+                    FRT_IDX_OK(s, (int64_t)((capacity + 3) >> 2) * (U >> 1) * 4);
+    w[j][0] = on ? __ldg(k_codes + c) : 0;
+    w[j][1] = on ? __ldg(v_codes + c) : 0;
+    f[j][0] = on ? __ldg(k_sf + s) : 0;
+    f[j][1] = on ? __ldg(v_sf + s) : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < kReadUnits; ++j) {
+    const int64_t at = at0 + j * kThreads;
+    if (slot[j] < 0 || !FRT_IDX_OK(at, total)) continue;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float sf = e4m3_value(f[j][t]);
+      uint32_t h[4], o[4];
+      e2m1x8_to_half2(w[j][t], h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = Pack16<FRT_F16>::to_float2(h[e]);
+        o[e] = Pack16<DT>::from_float2((v.x * sf) * gs[t], (v.y * sf) * gs[t]);
+      }
+      (t == 0 ? k_out : v_out)[at] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
 bool cache_ok(const void* k_codes, const void* k_sf, const void* v_codes, const void* v_sf, const void* kv_scales) {
@@ -354,9 +384,9 @@ extern "C" frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8
   if (!cache_ok(k_codes, k_sf, v_codes, v_sf, kv_scales) || k_out == nullptr || v_out == nullptr ||
       !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(slots, 4) || !aligned(status, 4))
     return FRT_ERR_INVALID_ARG;
-  const int64_t blocks = ((int64_t)n * Hkv * (hd / 8) + kThreads - 1) / kThreads;
+  const int64_t blocks = ((int64_t)n * Hkv * (hd / 8) + kThreads * kReadUnits - 1) / (kThreads * kReadUnits);
   if (blocks > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks, 2), block(kThreads);
+  const dim3 grid((unsigned)blocks), block(kThreads);
   return launch(dt == FRT_F16 ? read_kernel<FRT_F16> : read_kernel<FRT_BF16>, grid, block, 0, stream,
                 reinterpret_cast<const uint32_t*>(k_codes), k_sf, reinterpret_cast<const uint32_t*>(v_codes), v_sf,
                 kv_scales, slots, static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), status, n, Hkv, hd / 16,
