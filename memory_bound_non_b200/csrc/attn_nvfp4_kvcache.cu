@@ -29,8 +29,7 @@
 // beside V).  bf16 queries enter as binary16 times a power of two per row.
 #include <cmath>
 
-#include "frt_device.cuh"
-#include "frt_host.h"
+#include "attn_nvfp4.cuh"
 
 namespace frt {
 namespace {
@@ -39,101 +38,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;  // slots
 constexpr int kSMs = 148;
-
-struct Args {
-  const void* q;
-  const uint8_t* k_codes;
-  const uint8_t* k_sf;
-  const uint8_t* v_codes;
-  const uint8_t* v_sf;
-  const float* kv_scales;
-  const int32_t* kv_len;
-  const int32_t* q_indptr;
-  const int32_t* page_table;
-  void* out;
-  float2* part_ml;  // [chunk][M Hq] (maximum, sum)
-  float* part_o;    // [chunk][M Hq][hd]
-  int32_t* status;
-  int M, n_seqs, Hq, Hkv, hd, group;
-  int capacity, page_size, max_pages, n_pages;
-  int max_q_len, max_len;  // max_len: the largest length a token may have
-  int window;
-  uint32_t page_mul;  // p / page_size = (p + umulhi(p, page_mul)) >> page_shift
-  int page_shift;
-  int row_tiles, chunks, chunk_tiles;
-  float scale_log2;
-  int dt;
-};
-
-// Tokens [t0, t0 + n) of a sequence.
-struct Seq {
-  int t0, n;
-  bool bad;
-};
-__device__ __forceinline__ Seq sequence(const Args& a, int b) {
-  int s0 = 0, s1 = a.M;
-  if (a.q_indptr != nullptr && FRT_SPAN_OK(b, 2, a.n_seqs + 1)) {
-    s0 = __ldg(a.q_indptr + b);
-    s1 = __ldg(a.q_indptr + b + 1);
-  }
-  Seq s;
-  s.bad = s0 < 0 || s1 > a.M || s1 < s0;
-  s0 = min(max(s0, 0), a.M);
-  s1 = min(max(s1, s0), a.M);
-  s.t0 = s0;
-  s.n = s1 - s0;
-  if (s.n > a.max_q_len) {
-    s.n = a.max_q_len;
-    s.bad = true;
-  }
-  return s;
-}
-
-// The R query rows of a CTA (token-major, then the heads of the group) and the
-// positions they see.  Computed by every warp for itself, one row a lane (two
-// for R = 64).
-struct Rows {
-  int lo, hi;            // this lane's row: positions [lo, hi); empty: lo >= hi
-  int tok;               // its token, or -1
-  int head;              // its query head
-  int all_lo, all_hi;    // the positions that any row sees (empty: all_hi <= all_lo)
-  int full_lo, full_hi;  // the positions that every row sees
-  int tiles;             // kTile-slot tiles from first() on
-  bool bad;
-  __device__ __forceinline__ int first() const { return all_lo & ~3; }
-};
-template <int R>
-__device__ __forceinline__ Rows query_rows(const Args& a, int b, int rt, int kvh) {
-  static_assert(R <= 32, "one row a lane");
-  const Seq s = sequence(a, b);
-  const int lane = threadIdx.x & 31;
-  const int r = rt * R + lane;
-  Rows o;
-  o.bad = s.bad;
-  o.tok = -1;
-  o.head = 0;
-  o.lo = o.hi = 0;
-  if (lane < R && r / a.group < s.n) {
-    const int tok = s.t0 + r / a.group;
-    o.tok = tok;
-    o.head = kvh * a.group + r % a.group;
-    if (FRT_IDX_OK(tok, a.M)) {
-      const int len = __ldg(a.kv_len + tok);
-      o.hi = min(max(len, 0), a.max_len);
-      o.bad |= o.hi != len;
-      o.lo = a.window > 0 ? max(0, o.hi - a.window) : 0;
-    }
-  }
-  const bool sees = o.hi > o.lo;
-  o.all_lo = __reduce_min_sync(0xFFFFFFFFu, sees ? o.lo : 0x7FFFFFFF);
-  o.all_hi = __reduce_max_sync(0xFFFFFFFFu, sees ? o.hi : 0);
-  o.full_lo = __reduce_max_sync(0xFFFFFFFFu, o.tok >= 0 ? o.lo : 0);
-  o.full_hi = __reduce_min_sync(0xFFFFFFFFu, o.tok >= 0 ? o.hi : 0x7FFFFFFF);
-  if (o.all_hi <= o.all_lo) o.all_lo = o.all_hi = 0;
-  const int span = o.all_hi - o.first();
-  o.tiles = span / kTile + (span % kTile != 0);
-  return o;
-}
+using Args = AttnArgs;
 
 __device__ __forceinline__ uint32_t select_bits(uint32_t mask, uint32_t a, uint32_t b) {
   return (a & mask) | (b & ~mask);
@@ -160,22 +65,6 @@ struct Attn {
     uint32_t c[2][4][J];
     uint32_t sf[2][kVs];
   };
-
-  // First slot of the quad of positions pos .. pos + 3, or -1 (behind the end,
-  // or on a page that does not exist).
-  static __device__ __forceinline__ int quad_slot(const Args& a, int b, int pos, const Rows& rows) {
-    if (pos >= rows.all_hi) return -1;
-    if (a.page_table == nullptr) return pos;
-    const int page = (int)((__umulhi((uint32_t)pos, a.page_mul) + (uint32_t)pos) >> a.page_shift);
-    const int64_t at = (int64_t)b * a.max_pages + page;
-    if (!FRT_IDX_OK(at, (int64_t)a.n_seqs * a.max_pages)) return -1;
-    const int entry = __ldg(a.page_table + at);
-    if (entry < 0 || entry >= a.n_pages) {
-      if (a.status != nullptr && pos + 3 >= rows.all_lo) atomicOr(a.status, 1);
-      return -1;
-    }
-    return entry * a.page_size + (pos - page * a.page_size);
-  }
 
   // Where this lane's part of slot 0 lies; a slot's codes are row_bytes on, and
   // the factors of the quad that begins with slot s are s * sf_row on.  Blocks
@@ -295,11 +184,6 @@ struct Attn {
       if (sf_ok(a, sj, a.v_sf)) f.sf[h][j] = __ldg(reinterpret_cast<const uint32_t*>(sj));
     }
   }
-
-  // Bytes that hold the NaN factor, marked in their top bits.
-  static __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-  }
 };
 
 template <int HD, bool EXACT, int NT>
@@ -330,11 +214,14 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
   const int chunk = x / a.row_tiles;
 
   pdl_enter();
-  const Rows rows = query_rows<R>(a, b, rt, kvh);
+  const Seq seq = sequence(a, b);
+  const RowRange rows = row_range<R>(a, seq, rt * R, kvh);
   if (rows.bad && a.status != nullptr) atomicOr(a.status, 1);
+  const int tiles = rows.tiles(kTile);
   const int tile0 = chunk * a.chunk_tiles;
-  if (rows.full_hi == 0x7FFFFFFF || (chunk > 0 && tile0 >= rows.tiles)) return;  // no rows, or no work
-  const int tile1 = min(tile0 + a.chunk_tiles, rows.tiles);
+  if (!rows.any || (chunk > 0 && tile0 >= tiles)) return;  // no rows, or no work
+  const int tile1 = min(tile0 + a.chunk_tiles, tiles);
+  const QueryRow mine = query_row(a, seq, rt * R + lane, kvh);  // (lanes below R)
 
   const float gs_k = __ldg(a.kv_scales), gs_v = __ldg(a.kv_scales + 1);
 
@@ -344,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
   typename A::VFrag vf;
   int tile = tile0 + warp;
   auto position = [&](int tl) { return rows.first() + tl * kTile + 4 * g; };
-  auto slot_of = [&](int tl) { return tl < tile1 ? A::quad_slot(a, b, position(tl), rows) : -1; };
+  auto slot_of = [&](int tl) { return tl < tile1 ? quad_slot(a, b, position(tl), rows) : -1; };
   auto fetch_k = [&](int slot) { A::load_k(a, base, slot, kf); };
   auto fetch_v = [&](int slot) {
     A::load_v(a, base, 0, __shfl_sync(0xFFFFFFFFu, slot, 8 * t), vf);
@@ -357,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
 
   // queries: a warp a row, in the order that the lanes read them
   for (int r = warp; r < R; r += kWarps) {
-    const int tok = __shfl_sync(0xFFFFFFFFu, rows.tok, r), head = __shfl_sync(0xFFFFFFFFu, rows.head, r);
+    const int tok = __shfl_sync(0xFFFFFFFFu, mine.tok, r), head = __shfl_sync(0xFFFFFFFFu, mine.head, r);
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (tok >= 0 && lane < a.hd / 8) {
       const int64_t at = ((int64_t)tok * a.Hq + head) * (a.hd / 8) + lane;
@@ -395,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
       const int r = 8 * n + 2 * t + e;
       c[n][e] = q_scale[r];
       m[n][e] = -kInf;
-      lo[n][e] = __shfl_sync(0xFFFFFFFFu, rows.lo, r);
-      hi[n][e] = __shfl_sync(0xFFFFFFFFu, rows.hi, r);
+      lo[n][e] = __shfl_sync(0xFFFFFFFFu, mine.lo, r);
+      hi[n][e] = __shfl_sync(0xFFFFFFFFu, mine.hi, r);
     }
   float o[NT][HD / 16][4], l[NT][4];
 #pragma unroll
@@ -453,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < A::kVs; ++j) bad |= A::nan_bytes(vf.sf[h][j]);
+      for (int j = 0; j < A::kVs; ++j) bad |= nan_factors(vf.sf[h][j]);
     if (__any_sync(0xFFFFFFFFu, bad != 0)) {
       uint32_t nan_slots = 0;  // bit 8t + 4h + i
 #pragma unroll
@@ -461,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
         uint32_t mark = 0;
 #pragma unroll
         for (int j = 0; j < A::kVs; ++j) {
-          const uint32_t nb = A::nan_bytes(vf.sf[h][j]);
+          const uint32_t nb = nan_factors(vf.sf[h][j]);
           mark |= nb;
           vf.sf[h][j] &= ~((nb >> 7) * 0xFFu);
         }
@@ -599,15 +486,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
       if (g == 0) merge_l[warp * R + r] = l[n][e] * f;
     }
   __syncthreads();
-  const bool whole = rows.tiles <= a.chunk_tiles;  // this CTA saw all of the keys
+  const bool whole = tiles <= a.chunk_tiles;  // this CTA saw all of the keys
   const int quarter = a.hd / 4;
   for (int i = threadIdx.x; i < R * quarter; i += kThreads) {
     const int r = i / quarter, d = (i - r * quarter) * 4;
-    // row r's token and head, as query_rows gives them
-    const int rr = rt * R + r;
-    const Seq sq = sequence(a, b);
-    if (rr / a.group >= sq.n) continue;
-    const int64_t row = (int64_t)(sq.t0 + rr / a.group) * a.Hq + kvh * a.group + rr % a.group;
+    const int rr = rt * R + r, tok = rr / a.group;
+    if (tok >= seq.n) continue;
+    const int64_t row = (int64_t)(seq.t0 + tok) * a.Hq + kvh * a.group + (rr - tok * a.group);
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sum = 0.0f;
 #pragma unroll
@@ -619,25 +504,16 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
       v.w += u.w;
       sum += merge_l[w * R + r];
     }
-    const int64_t at = row * a.hd + d;
     if (whole) {
-      const float f = sum == 0.0f ? 0.0f : gs_v / sum;
-      const uint2 w = a.dt == FRT_F16 ? make_uint2(Pack16<FRT_F16>::from_float2(v.x * f, v.y * f),
-                                                   Pack16<FRT_F16>::from_float2(v.z * f, v.w * f))
-                                      : make_uint2(Pack16<FRT_BF16>::from_float2(v.x * f, v.y * f),
-                                                   Pack16<FRT_BF16>::from_float2(v.z * f, v.w * f));
-      if (FRT_SPAN_OK(at, 4, (int64_t)a.M * a.Hq * a.hd))
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = w;
+      store_out4(a, row * a.hd + d, v, sum == 0.0f ? 0.0f : gs_v / sum);
     } else {
-      const int64_t n_rows = (int64_t)a.M * a.Hq;
-      const int64_t part = (int64_t)chunk * n_rows;
-      if (FRT_SPAN_OK(part * a.hd + at, 4, n_rows * a.chunks * a.hd))
-        *reinterpret_cast<float4*>(a.part_o + part * a.hd + at) = v;
-      if (d == 0 && FRT_IDX_OK(part + row, n_rows * a.chunks)) {
+      store_part4(a, chunk, row * a.hd + d, v);
+      const int64_t at = (int64_t)chunk * a.M * a.Hq + row;
+      if (d == 0 && FRT_IDX_OK(at, (int64_t)a.M * a.Hq * a.chunks)) {
         float top = merge_m[r];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_m[w * R + r]);
-        a.part_ml[part + row] = make_float2(top, sum);
+        a.part_ml[at] = make_float2(top, sum);
       }
     }
   }
@@ -647,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
 // every other chunk, in a fixed order.
 constexpr int kJoinThreads = 256;
 template <int R>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int keys) {
   __shared__ float4 sums[kJoinThreads];
   const int b = blockIdx.y;
   int x = blockIdx.x;
@@ -656,11 +532,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   const int kvh = x % a.Hkv;
   const int rt = x / a.Hkv;
   pdl_enter();
-  const Rows rows = query_rows<R>(a, b, rt, kvh);
-  const int tok = __shfl_sync(0xFFFFFFFFu, rows.tok, r), head = __shfl_sync(0xFFFFFFFFu, rows.head, r);
-  const int n = (rows.tiles + a.chunk_tiles - 1) / a.chunk_tiles;
-  if (tok < 0 || n <= 1) return;
-  const int64_t n_rows = (int64_t)a.M * a.Hq, row = (int64_t)tok * a.Hq + head;
+  const Seq seq = sequence(a, b);
+  const QueryRow mine = query_row(a, seq, rt * R + r, kvh);
+  if (mine.tok < 0) return;
+  const int n = (row_range<R>(a, seq, rt * R, kvh).tiles(keys) + a.chunk_tiles - 1) / a.chunk_tiles;
+  if (n <= 1) return;
+  const int64_t n_rows = (int64_t)a.M * a.Hq, row = (int64_t)mine.tok * a.Hq + mine.head;
   const float kInf = __int_as_float(0x7F800000);
   const int lane = threadIdx.x & 31;
   float top = -kInf;
@@ -704,34 +581,80 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
     v.z += u.z;
     v.w += u.w;
   }
-  const float f = sum == 0.0f ? 0.0f : __ldg(a.kv_scales + 1) / sum;
-  const uint2 w = a.dt == FRT_F16 ? make_uint2(Pack16<FRT_F16>::from_float2(v.x * f, v.y * f),
-                                               Pack16<FRT_F16>::from_float2(v.z * f, v.w * f))
-                                  : make_uint2(Pack16<FRT_BF16>::from_float2(v.x * f, v.y * f),
-                                               Pack16<FRT_BF16>::from_float2(v.z * f, v.w * f));
-  if (FRT_SPAN_OK(row * a.hd + d, 4, n_rows * a.hd))
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.hd + d) = w;
+  store_out4(a, row * a.hd + d, v, sum == 0.0f ? 0.0f : __ldg(a.kv_scales + 1) / sum);
 }
 
-// How a call is cut: NT x 8 query rows to a CTA, and the keys into chunks.
+// The same with a warp to a row, for many rows and few chunks each.
+constexpr int kJoinRows = kJoinThreads / 32;
+__global__ void __launch_bounds__(kJoinThreads) join_rows_kernel(const Args a, int keys) {
+  static_assert(kTileRows % kJoinRows == 0, "a CTA's rows lie in one row tile");
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  int x = blockIdx.x;
+  const int r = x % (kTileRows / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
+  x /= kTileRows / kJoinRows;
+  const int kvh = x % a.Hkv;
+  const int rt = x / a.Hkv;
+  pdl_enter();
+  const Seq seq = sequence(a, b);
+  const QueryRow mine = query_row(a, seq, rt * kTileRows + r, kvh);
+  const int n = (row_range<kTileRows>(a, seq, rt * kTileRows, kvh).tiles(keys) + a.chunk_tiles - 1) / a.chunk_tiles;
+  if (mine.tok < 0 || n <= 1) return;
+  const int64_t n_rows = (int64_t)a.M * a.Hq, row = (int64_t)mine.tok * a.Hq + mine.head;
+  const float kInf = __int_as_float(0x7F800000);
+  float top = -kInf;
+  for (int i = 0; i < n; ++i)
+    if (FRT_IDX_OK(i * n_rows + row, n_rows * a.chunks)) top = fmaxf(top, a.part_ml[i * n_rows + row].x);
+  float sum = 0.0f;
+  float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  for (int i = 0; i < n; ++i) {
+    if (!FRT_IDX_OK(i * n_rows + row, n_rows * a.chunks)) continue;
+    const float2 ml = a.part_ml[i * n_rows + row];
+    const float f = ml.x == -kInf ? 0.0f : ex2_approx(ml.x - top);
+    sum += ml.y * f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int d = 128 * h + 4 * lane;
+      const int64_t at = (i * n_rows + row) * a.hd + d;
+      if (d >= a.hd || !FRT_SPAN_OK(at, 4, n_rows * a.chunks * a.hd)) continue;
+      const float4 u = *reinterpret_cast<const float4*>(a.part_o + at);
+      v[h].x = fmaf(u.x, f, v[h].x);
+      v[h].y = fmaf(u.y, f, v[h].y);
+      v[h].z = fmaf(u.z, f, v[h].z);
+      v[h].w = fmaf(u.w, f, v[h].w);
+    }
+  }
+  const float f = sum == 0.0f ? 0.0f : __ldg(a.kv_scales + 1) / sum;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (128 * h + 4 * lane < a.hd) store_out4(a, row * a.hd + 128 * h + 4 * lane, v[h], f);
+}
+
+// How a call is cut: the rows of a CTA (8 nt, or the tile kernel's), and the
+// keys into chunks of chunk_tiles tiles.
 struct Plan {
-  int nt, row_tiles, chunks, chunk_tiles;
+  int nt;  // 0: the tile kernel
+  int row_tiles, chunks, chunk_tiles, keys;
 };
+// From this many rows of a sequence and KV head on the tile kernel takes them.
+constexpr int64_t kManyRows = 48;
 Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
   Plan p;
   const int64_t rows = (int64_t)max_q_len * (Hq / Hkv);
-  p.nt = rows <= 8 ? 1 : rows <= 16 || hd > 128 ? 2 : 4;
-  const int64_t row_tiles = (rows + 8 * p.nt - 1) / (8 * p.nt);
+  p.nt = rows >= kManyRows ? 0 : rows <= 8 ? 1 : rows <= 16 || hd > 128 ? 2 : 4;
+  const int tile_rows = p.nt == 0 ? kTileRows : 8 * p.nt;
+  p.keys = p.nt == 0 ? tile_keys(hd) : kTile;
+  const int64_t row_tiles = (rows + tile_rows - 1) / tile_rows;
   p.row_tiles = (int)(row_tiles > 0x7FFFFFFF ? 0x7FFFFFFF : row_tiles);
-  const int64_t tiles = ((int64_t)max_kv_len + 3) / kTile + 1;
+  const int64_t tiles = ((int64_t)max_kv_len + 3) / p.keys + 1;
   const int64_t ctas = row_tiles * Hkv * n_seqs;
   // enough CTAs for one full wave; a batch of sequences, whose lengths
   // differ, gets four
-  const int64_t want = (int64_t)kSMs * 4 * (n_seqs > 1 ? 4 : 1);
+  const int64_t resident = p.nt == 0 ? (hd > 192 ? 1 : 2) : 4;
+  const int64_t want = (int64_t)kSMs * resident * (n_seqs > 1 ? 4 : 1);
   int64_t chunks = want / (ctas > 0 ? ctas : 1);
   chunks = chunks < 1 ? 1 : chunks;
   int64_t per = (tiles + chunks - 1) / chunks;
-  per = (per + kWarps - 1) / kWarps * kWarps;
+  if (p.nt != 0) per = (per + kWarps - 1) / kWarps * kWarps;
   p.chunk_tiles = (int)per;
   p.chunks = (int)((tiles + per - 1) / per);
   return p;
@@ -748,14 +671,8 @@ frt_status launch_attn(const Args& a, cudaStream_t stream) {
   static std::atomic<int> opted{48 * 1024};
   const frt_status st = opt_in_smem(attn_kernel<HD, EXACT, NT>, A::kSmem, opted);
   if (st != FRT_OK) return st;
-  const int64_t gx = (int64_t)a.Hkv * a.row_tiles * a.chunks;
-  if (gx > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
-  const frt_status s1 = launch(attn_kernel<HD, EXACT, NT>, dim3((unsigned)gx, a.n_seqs), dim3(kThreads), A::kSmem,
-                               stream, a);
-  if (s1 != FRT_OK || a.chunks == 1) return s1;
-  const int64_t jx = (int64_t)a.Hkv * a.row_tiles * A::R;
-  if (jx > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
-  return launch(join_kernel<A::R>, dim3((unsigned)jx, a.n_seqs), dim3(kJoinThreads), 0, stream, a);
+  return launch(attn_kernel<HD, EXACT, NT>, dim3((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), dim3(kThreads),
+                A::kSmem, stream, a);
 }
 template <int HD, int NT>
 frt_status launch_exact(const Args& a, cudaStream_t stream) {
@@ -849,5 +766,17 @@ extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_cod
   a.chunk_tiles = p.chunk_tiles;
   a.scale_log2 = softmax_scale * kLog2e;
   a.dt = dt;
-  return p.nt == 1 ? launch_hd<1>(a, stream) : p.nt == 2 ? launch_hd<2>(a, stream) : launch_hd<4>(a, stream);
+  const int rows = p.nt == 0 ? kTileRows : 8 * p.nt;
+  if ((int64_t)Hkv * p.row_tiles * (p.chunks > rows ? p.chunks : rows) > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
+  const frt_status st = p.nt == 0   ? launch_attn_tiles(a, stream)
+                        : p.nt == 1 ? launch_hd<1>(a, stream)
+                        : p.nt == 2 ? launch_hd<2>(a, stream)
+                                    : launch_hd<4>(a, stream);
+  if (st != FRT_OK || a.chunks == 1) return st;
+  const dim3 grid((unsigned)(Hkv * p.row_tiles * (p.nt == 0 ? rows / kJoinRows : rows)), n_seqs), block(kJoinThreads);
+  return launch(p.nt == 0   ? join_rows_kernel
+                : p.nt == 1 ? join_kernel<8>
+                : p.nt == 2 ? join_kernel<16>
+                            : join_kernel<32>,
+                grid, block, 0, stream, a, p.keys);
 }

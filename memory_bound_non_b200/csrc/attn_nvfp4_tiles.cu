@@ -1,0 +1,458 @@
+// Attention over an NVFP4 KV cache for many query rows (a chunk of a prefill, a
+// wide group): 128 rows of one KV head to a CTA, on the 5th-generation tensor
+// cores.
+//
+// What bounds it: 4 hd operations per row and key on the tensor cores and one
+// exponential per row and key on the special-function units (16 a clock and
+// SM: 1024 clocks for a tile of 128 x 128, the products take 1024 together at
+// hd 128); the cache is read from L2 by the row tiles of a head.
+//
+// One tile of KT keys:
+//   K codes -> binary16 in shared memory (all warps)      | P V of the tile before
+//   S = Q K^T                        (tcgen05, S in TMEM)  | V codes -> binary16
+//   p = 2^(s - m + 11) in registers, two threads a row
+//   P -> TMEM (binary16, over S), O += P V  (tcgen05, P from TMEM, O in TMEM)
+// Two CTAs share an SM (hd <= 192), so that one's products run beside the
+// other's conversions and exponentials; that is all the pipelining there is.
+//
+// Operand layouts: Q and K as rows of 64 dimensions (128 bytes) with the
+// 128-byte swizzle, k-major; V in the same form, which read as the B operand of
+// P V is mn-major (dimensions contiguous, keys eight to a group of 1024 bytes).
+// The 16-byte pieces are written by lanes that hold 4 blocks of 2 keys, which
+// is free of bank conflicts.
+//
+// m is renewed when a score passes it by more than 4 (as in the kernel for few
+// rows); O is then rescaled in TMEM.  c >= 0: a negative scale is moved into Q.
+#include "attn_nvfp4.cuh"
+
+namespace frt {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kQRegion = kTileRows * 128;  // bytes of 64 dimensions of all rows
+
+template <int HD>
+struct Tile {
+  static constexpr int C = HD / 64;          // regions of 64 dimensions
+  static constexpr int KT = tile_keys(HD);   // keys
+  static constexpr int kRegion = KT * 128;   // bytes of 64 dimensions of all keys
+  static constexpr int U = KT * C / 64;      // 16-element blocks a thread converts
+  static constexpr int kCols = KT + HD <= 256 ? 256 : 512;  // TMEM columns: S (P over it), O
+  static constexpr int kO = KT;                             // first column of O
+  static constexpr size_t kSmem = 1024 + C * (kQRegion + 2 * kRegion) + 4096;
+};
+
+// ------------------------------------------------------------ tcgen05 --
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <int COLS>
+__device__ __forceinline__ void tc_alloc(uint32_t* where) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)), "n"(COLS)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+template <int COLS>
+__device__ __forceinline__ void tc_free(uint32_t tmem) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS));
+}
+// Arrives on the barrier when this thread's products so far are done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+// 32 columns of this thread's lane
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+// Shared-memory operand with the 128-byte swizzle: bits 0-13 address / 16, 16-29
+// and 32-45 the leading and stride byte offsets / 16, 46-48 = 1, 61-63 = 2.
+__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, int leading, int stride) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+// fp32 sums of binary16 products, 128 rows by N columns; b_mn: B is mn-major
+__host__ __device__ constexpr uint32_t product_desc(int n, bool b_mn) {
+  return 1u << 4 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+__device__ __forceinline__ void tc_mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      : "memory");
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+struct Small {  // behind the operands
+  float top[2][kTileRows];    // each half's largest score of a row; at the end its sum
+  float scale[kTileRows];     // score -> log2 units
+  int tok[kTileRows], head[kTileRows];
+  int slot[2][32];            // quad slots of a tile, by tile parity
+  int holes[2];               // a tile has quads that are not there
+  uint32_t nan[4];            // keys of the tile with a NaN factor in V
+  uint64_t s_done, o_done;
+  uint32_t tmem;
+  int gave_up;
+};
+static_assert(sizeof(Small) <= 4096, "fits behind the operands");
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const AttnArgs a, int polls) {
+  using T = Tile<HD>;
+  constexpr int C = T::C, KT = T::KT, U = T::U, kRegion = T::kRegion;
+  extern __shared__ unsigned char raw_smem[];
+  const uint32_t base = (smem_addr(raw_smem) + 1023) & ~1023u;
+  const uint32_t q_smem = base, k_smem = base + C * kQRegion, v_smem = k_smem + C * kRegion;
+  Small& sm = *reinterpret_cast<Small*>(raw_smem + (v_smem + C * kRegion - smem_addr(raw_smem)));
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.y;
+  int x = blockIdx.x;
+  const int kvh = x % a.Hkv;
+  x /= a.Hkv;
+  const int rt = x % a.row_tiles;
+  const int chunk = x / a.row_tiles;
+
+  pdl_enter();
+  const Seq seq = sequence(a, b);
+  const RowRange range = row_range<kTileRows>(a, seq, rt * kTileRows, kvh);
+  if (range.bad && a.status != nullptr) atomicOr(a.status, 1);
+  const int tiles = range.tiles(KT);
+  const int tile0 = chunk * a.chunk_tiles;
+  if (!range.any || (chunk > 0 && tile0 >= tiles)) return;  // no rows, or no work
+  const int tile1 = min(tile0 + a.chunk_tiles, tiles);
+
+  // this thread's row and half of the columns (TMEM lanes are split by warp % 4)
+  const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+  const QueryRow mine = query_row(a, seq, rt * kTileRows + row, kvh);
+  if (half == 0) {
+    sm.tok[row] = mine.tok;
+    sm.head[row] = mine.head;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.s_done, 1);
+    mbar_init(&sm.o_done, 1);
+    mbar_init_fence();
+    sm.gave_up = 0;
+  }
+  if (warp == 0) {
+    __syncwarp();
+    tc_alloc<T::kCols>(&sm.tmem);
+  }
+
+  const int nblk = a.hd >> 4;
+  auto find_slots = [&](int tile) {  // warp 0
+    const int slot = tile < tile1 && lane < KT / 4 ? quad_slot(a, b, range.first() + tile * KT + 4 * lane, range) : -1;
+    sm.slot[tile & 1][lane] = slot;
+    const bool hole = __any_sync(0xFFFFFFFFu, lane < KT / 4 && slot < 0);
+    if (lane == 0) sm.holes[tile & 1] = hole;
+  };
+  if (warp == 0) find_slots(tile0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const uint32_t s_tmem = tmem + ((uint32_t)(warp & 3) << 21), o_tmem = s_tmem + T::kO;
+
+  // The blocks that this thread converts: of unit i key key_of(i), region
+  // kc_of(i), block 4 kc + lane % 4.
+  auto kc_of = [&](int i) { return (warp * 4 + (lane >> 3) + 32 * i) % C; };
+  auto key_of = [&](int i) { return 2 * ((warp * 4 + (lane >> 3) + 32 * i) / C) + ((lane >> 2) & 1); };
+  struct Raw {
+    uint2 c[U];
+    uint32_t sf[U];
+  };
+  const int row_bytes = a.Hkv * (a.hd >> 1);
+  auto load = [&](const uint8_t* codes, const uint8_t* sf, int tile, Raw& r) {
+    const int left = range.all_hi - (range.first() + tile * KT);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int key = key_of(i), blk = 4 * kc_of(i) + (lane & 3);
+      const int quad = tile < tile1 ? sm.slot[tile & 1][key >> 2] : -1;
+      r.c[i] = make_uint2(0, 0);
+      r.sf[i] = 0;
+      if (quad >= 0 && key < left && blk < nblk) {
+        const int64_t at = (int64_t)(quad + (key & 3)) * row_bytes + kvh * (a.hd >> 1) + 8 * blk;
+        const int64_t s = (int64_t)quad * (a.Hkv * nblk) + (kvh * nblk + blk) * 4 + (key & 3);
+        if (FRT_SPAN_OK(at, 8, (int64_t)a.capacity * row_bytes))
+          r.c[i] = ld_stream(reinterpret_cast<const uint2*>(codes + at));
+        if (FRT_IDX_OK(s, (int64_t)((a.capacity + 3) >> 2) * a.Hkv * nblk * 4)) r.sf[i] = __ldg(sf + s);
+      }
+    }
+  };
+  auto convert = [&](const Raw& r, uint32_t to, bool is_v) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int key = key_of(i);
+      uint32_t sf = r.sf[i];
+      if (is_v && (sf & 0x7F) == 0x7F) {
+        sf = 0;
+        atomicOr(&sm.nan[key >> 5], 1u << (key & 31));
+      }
+      uint32_t f[2], h[8];
+      e4m3x4_to_half2(sf * 0x0101u, f);
+      e2m1x8_to_half2(r.c[i].x, h);
+      e2m1x8_to_half2(r.c[i].y, h + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = hmul2(h[e], f[0]);
+      const uint32_t line = to + kc_of(i) * kRegion + key * 128;
+      const int piece = 2 * (lane & 3);
+      st_shared16(line + ((piece ^ (key & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+      st_shared16(line + (((piece + 1) ^ (key & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+    }
+  };
+  bool gave_up = false;
+  auto wait = [&](uint64_t* bar, int phase) {
+    if (!gave_up && !mbar_wait_bounded(bar, phase, polls)) {
+      gave_up = true;
+      sm.gave_up = 1;
+    }
+  };
+
+  Raw k_raw;
+  load(a.k_codes, a.k_sf, tile0, k_raw);
+
+  // ---- Q: 16 lanes a row (32 above 128 dimensions)
+  {
+    constexpr int kLanes = HD <= 128 ? 16 : 32, kRows = 32 / kLanes;
+    const float c = a.scale_log2 * __ldg(a.kv_scales);
+    const uint32_t flip = c < 0.0f ? 0x80008000u : 0u;
+    const int l = lane % kLanes;
+#pragma unroll 4
+    for (int i = 0; i < kTileRows / (8 * kRows); ++i) {
+      const int r = (i * 8 + warp) * kRows + lane / kLanes;
+      const int tok = sm.tok[r];
+      uint4 v = make_uint4(0, 0, 0, 0);
+      const int64_t at = ((int64_t)tok * a.Hq + sm.head[r]) * (a.hd / 8) + l;
+      if (tok >= 0 && l < a.hd / 8 && FRT_IDX_OK(at, (int64_t)a.M * a.Hq * (a.hd / 8)))
+        v = ld_plain(static_cast<const uint4*>(a.q) + at);
+      float s = 1.0f;
+      if (a.dt == FRT_BF16) {
+        float2 f[4];
+        unpack_pairs<FRT_BF16, 4>(&v.x, f);
+        const float amax = fmaxf(absmax4(f[0].x, f[0].y, f[1].x, f[1].y), absmax4(f[2].x, f[2].y, f[3].x, f[3].y));
+        s = pow2_to_half_range(kLanes == 16 ? half_warp_max_abs(amax) : warp_max_abs(amax));
+        mul_pairs<4>(f, s);
+        pack_pairs<FRT_F16, 4>(f, &v.x);
+      }
+      v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+      if (l < HD / 8) st_shared16(q_smem + (l >> 3) * kQRegion + r * 128 + (((l & 7) ^ (r & 7)) << 4), v);
+      // (never 0, which would make a masked score NaN)
+      if (l == 0) sm.scale[r] = fmaxf(fabsf(c) / s, 0x1p-120f);
+    }
+  }
+
+  const float kInf = __int_as_float(0x7F800000);
+  float m = -kInf, sum = 0.0f;
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const int nth = tile - tile0;
+    Raw v_raw;
+    load(a.v_codes, a.v_sf, tile, v_raw);
+    if (warp == 0) find_slots(tile + 1);
+    if (threadIdx.x < 4) sm.nan[threadIdx.x] = 0;
+    convert(k_raw, k_smem, false);
+    fence_proxy_async_smem();
+    if (nth > 0) wait(&sm.o_done, (nth - 1) & 1);  // V and P of the tile before are read
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k)
+        tc_mma_smem(tmem, smem_operand(q_smem + (k >> 2) * kQRegion + (k & 3) * 32, 16, 1024),
+                    smem_operand(k_smem + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024), product_desc(KT, false), k > 0);
+      tc_commit(&sm.s_done);
+    }
+    __syncwarp();
+    convert(v_raw, v_smem, true);
+    fence_proxy_async_smem();
+    load(a.k_codes, a.k_sf, tile + 1, k_raw);
+
+    wait(&sm.s_done, nth & 1);
+    tc_fence_after();
+    uint32_t s[KT / 2];
+#pragma unroll
+    for (int i = 0; i < KT / 64; ++i) tc_ld32(s_tmem + half * (KT / 2) + 32 * i, s + 32 * i);
+    tc_wait_ld();
+    // masks
+    const int pos = range.first() + tile * KT + half * (KT / 2);
+    const int pos0 = range.first() + tile * KT;
+    if (pos0 < range.full_lo || range.full_hi - pos0 < KT || sm.holes[tile & 1] != 0) {
+      const int from = mine.lo - pos, to = mine.hi - pos;
+#pragma unroll
+      for (int i = 0; i < KT / 2; ++i) {
+        const bool there = sm.slot[tile & 1][(half * (KT / 2) + i) >> 2] >= 0;
+        if (i < from || i >= to || !there) s[i] = 0xFF800000u;
+      }
+    }
+    float top = __uint_as_float(s[0]);
+#pragma unroll
+    for (int i = 1; i < KT / 2; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+    sm.top[half][row] = top;
+    tc_fence_before();
+    __syncthreads();
+    const float c = sm.scale[row];
+    top = fmaxf(top, sm.top[half ^ 1][row]) * c;
+    // a NaN factor in V: the weight of its key turns NaN for the rows that see it
+#pragma unroll
+    for (int w = 0; w < KT / 64; ++w) {
+      const uint32_t nan = sm.nan[half * (KT / 64) + w];
+      if (nan != 0) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if ((nan >> i & 1) && s[32 * w + i] != 0xFF800000u) s[32 * w + i] = 0x7FC00000u;
+      }
+    }
+    const bool renew = top > m + 4.0f;
+    float f = 1.0f;
+    if (renew) {
+      f = ex2_approx(m - top);
+      m = top;
+      sum *= f;
+    }
+    __syncwarp();
+    tc_fence_after();
+    if (nth > 0 && __any_sync(0xFFFFFFFFu, renew)) {
+#pragma unroll 1
+      for (int i = 0; i < HD / 64; ++i) {
+        uint32_t o[32];
+        const uint32_t at = o_tmem + half * (HD / 2) + 32 * i;
+        tc_ld32(at, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tc_st32(at, o);
+      }
+    }
+    const float shift = 11.0f - (m == -kInf ? 0.0f : m);
+    uint32_t p[KT / 4];
+#pragma unroll
+    for (int i = 0; i < KT / 4; ++i) {
+      p[i] = Pack16<FRT_F16>::from_float2(ex2_approx(fmaf(__uint_as_float(s[2 * i]), c, shift)),
+                                          ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), c, shift)));
+      const float2 u = Pack16<FRT_F16>::to_float2(p[i]);
+      sum += u.x + u.y;
+    }
+    if constexpr (KT == 128)
+      tc_st32(s_tmem + half * 32, p);
+    else
+      tc_st16(s_tmem + half * 16, p);
+    tc_wait_st();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < KT / 16; ++k)
+        tc_mma_tmem(tmem + T::kO, tmem + 8 * k, smem_operand(v_smem + k * 2048, kRegion, 1024),
+                    product_desc(HD, true), nth > 0 || k > 0);
+      tc_commit(&sm.o_done);
+    }
+    __syncwarp();
+  }
+
+  // ---- output
+  const int n = tile1 - tile0;
+  if (n > 0) wait(&sm.o_done, (n - 1) & 1);
+  sm.top[half][row] = sum;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  sum += sm.top[half ^ 1][row];
+  const bool whole = tiles <= a.chunk_tiles;  // this CTA saw all of the keys
+  const float f = !whole ? 1.0f : sum == 0.0f ? 0.0f : __ldg(a.kv_scales + 1) / sum;
+  const int64_t q_row = (int64_t)mine.tok * a.Hq + mine.head;
+#pragma unroll 1
+  for (int i = 0; i < HD / 64; ++i) {
+    uint32_t o[32];
+    const int d0 = half * (HD / 2) + 32 * i;
+    if (n > 0) {
+      tc_ld32(o_tmem + d0, o);
+      tc_wait_ld();
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      if (mine.tok < 0 || d0 + e >= a.hd) continue;
+      const float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                   __uint_as_float(o[e + 3]));
+      if (whole)
+        store_out4(a, q_row * a.hd + d0 + e, v, f);
+      else
+        store_part4(a, chunk, q_row * a.hd + d0 + e, v);
+    }
+    __syncwarp();
+  }
+  if (!whole && mine.tok >= 0 && half == 0) {
+    const int64_t at = (int64_t)chunk * a.M * a.Hq + q_row;
+    if (FRT_IDX_OK(at, (int64_t)a.M * a.Hq * a.chunks)) a.part_ml[at] = make_float2(m, sum);
+  }
+  // a wait that ran out: report it, and let the products end before TMEM is freed
+  if (sm.gave_up != 0 && threadIdx.x == 0) {
+    if (a.status != nullptr) atomicOr(a.status, 2);
+    if (n > 0) (void)mbar_wait_bounded(&sm.o_done, (n - 1) & 1, 1 << 16);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tc_free<T::kCols>(tmem);
+}
+
+template <int HD>
+frt_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
+  static std::atomic<int> opted{48 * 1024};
+  const frt_status st = opt_in_smem(tiles_kernel<HD>, Tile<HD>::kSmem, opted);
+  if (st != FRT_OK) return st;
+  return launch(tiles_kernel<HD>, dim3((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), dim3(kThreads),
+                Tile<HD>::kSmem, stream, a, wait_polls());
+}
+
+}  // namespace
+
+frt_status launch_attn_tiles(const AttnArgs& a, cudaStream_t stream) {
+  return a.hd <= 64    ? launch_tiles<64>(a, stream)
+         : a.hd <= 128 ? launch_tiles<128>(a, stream)
+         : a.hd <= 192 ? launch_tiles<192>(a, stream)
+                       : launch_tiles<256>(a, stream);
+}
+
+}  // namespace frt
