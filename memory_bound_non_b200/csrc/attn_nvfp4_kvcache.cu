@@ -55,7 +55,7 @@ struct Attn {
   static constexpr int kOStride = HD + 4;
   static constexpr size_t kQBytes = (size_t)kSteps * NT * 32 * 8;
   static constexpr size_t kMergeBytes = (size_t)kWarps * R * kOStride * 4;
-  static constexpr size_t kSmem = (kQBytes > kMergeBytes ? kQBytes : kMergeBytes) + R * 4 + 2 * kWarps * R * 4;
+  static constexpr size_t kSmem = (kQBytes > kMergeBytes ? kQBytes : kMergeBytes) + R * 4 + 2 * kWarps * R * 4 + R * 8 + 8 * R * 4;
 
   struct KFrag {
     uint32_t c[4][2 * J];
@@ -198,29 +198,26 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
   extern __shared__ __align__(16) unsigned char smem[];
   uint2* q_frag = reinterpret_cast<uint2*>(smem);
   float* merge_o = reinterpret_cast<float*>(smem);
-  float* q_scale = reinterpret_cast<float*>(smem + A::kSmem - R * 4 - 2 * kWarps * R * 4);
+  float* q_scale = reinterpret_cast<float*>(smem + A::kSmem - R * 4 - 2 * kWarps * R * 4 - R * 8 - 8 * R * 4);
   float* merge_m = q_scale + R;
   float* merge_l = merge_m + kWarps * R;
+  float2* cta_ml = reinterpret_cast<float2*>(merge_l + kWarps * R);
+  float* factor = reinterpret_cast<float*>(cta_ml + R);  // [8][R]
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int b = blockIdx.y;
-  // heads are neighbours in the grid: CTAs that run at the same time read
-  // neighbouring bytes of a slot
-  int x = blockIdx.x;
-  const int kvh = x % a.Hkv;
-  x /= a.Hkv;
-  const int rt = x % a.row_tiles;
-  const int chunk = x / a.row_tiles;
+  const Place place = place_of(a);
+  const int kvh = place.kvh, rt = place.rt, chunk = place.chunk;
 
   pdl_enter();
   const Seq seq = sequence(a, b);
   const RowRange rows = row_range<R>(a, seq, rt * R, kvh);
   if (rows.bad && a.status != nullptr) atomicOr(a.status, 1);
   const int tiles = rows.tiles(kTile);
-  const int tile0 = chunk * a.chunk_tiles;
-  if (!rows.any || (chunk > 0 && tile0 >= tiles)) return;  // no rows, or no work
-  const int tile1 = min(tile0 + a.chunk_tiles, tiles);
+  const int2 part = tiles_of(a, chunk, tiles);
+  const int tile0 = part.x, tile1 = part.y;
+  if (!rows.any || (!a.cluster && chunk > 0 && tile0 >= tiles)) return;  // no rows, or no work
   const QueryRow mine = query_row(a, seq, rt * R + lane, kvh);  // (lanes below R)
 
   const float gs_k = __ldg(a.kv_scales), gs_v = __ldg(a.kv_scales + 1);
@@ -243,30 +240,35 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
   fetch_v(slot);
 
   // queries: a warp a row, in the order that the lanes read them
-  for (int r = warp; r < R; r += kWarps) {
+  constexpr int kEach = R / kWarps;
+  uint4 raw[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int r = warp + kWarps * i;
     const int tok = __shfl_sync(0xFFFFFFFFu, mine.tok, r), head = __shfl_sync(0xFFFFFFFFu, mine.head, r);
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (tok >= 0 && lane < a.hd / 8) {
-      const int64_t at = ((int64_t)tok * a.Hq + head) * (a.hd / 8) + lane;
-      if (FRT_IDX_OK(at, (int64_t)a.M * a.Hq * (a.hd / 8))) raw = ld_plain(static_cast<const uint4*>(a.q) + at);
-    }
+    const int64_t at = ((int64_t)tok * a.Hq + head) * (a.hd / 8) + lane;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (tok >= 0 && lane < a.hd / 8 && FRT_IDX_OK(at, (int64_t)a.M * a.Hq * (a.hd / 8)))
+      raw[i] = ld_plain(static_cast<const uint4*>(a.q) + at);
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int r = warp + kWarps * i;
     float s = 1.0f;
     if (a.dt == FRT_BF16) {
       float2 v[4];
-      unpack_pairs<FRT_BF16, 4>(&raw.x, v);
-      float amax = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
+      unpack_pairs<FRT_BF16, 4>(&raw[i].x, v);
+      const float amax = fmaxf(absmax4(v[0].x, v[0].y, v[1].x, v[1].y), absmax4(v[2].x, v[2].y, v[3].x, v[3].y));
       s = pow2_to_half_range(warp_max_abs(amax));
       mul_pairs<4>(v, s);
-      pack_pairs<FRT_F16, 4>(v, &raw.x);
+      pack_pairs<FRT_F16, 4>(v, &raw[i].x);
     }
     if (lane < HD / 8) {
       const int blk = lane >> 1;
       const int step = (blk % J) * 4 + (lane & 1) * 2;
       uint2* dst = q_frag + ((step * NT + (r >> 3)) * 32 + (r & 7) * 4 + blk / J);
-      dst[0] = make_uint2(raw.x, raw.y);
-      dst[NT * 32] = make_uint2(raw.z, raw.w);
+      dst[0] = make_uint2(raw[i].x, raw[i].y);
+      dst[NT * 32] = make_uint2(raw[i].z, raw[i].w);
     }
     if (lane == 0) q_scale[r] = a.scale_log2 * gs_k / s;
   }
@@ -486,178 +488,203 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
       if (g == 0) merge_l[warp * R + r] = l[n][e] * f;
     }
   __syncthreads();
-  const bool whole = tiles <= a.chunk_tiles;  // this CTA saw all of the keys
-  const int quarter = a.hd / 4;
-  for (int i = threadIdx.x; i < R * quarter; i += kThreads) {
-    const int r = i / quarter, d = (i - r * quarter) * 4;
-    const int rr = rt * R + r, tok = rr / a.group;
-    if (tok >= seq.n) continue;
-    const int64_t row = (int64_t)(seq.t0 + tok) * a.Hq + kvh * a.group + (rr - tok * a.group);
+  const bool whole = !a.cluster && tiles <= a.chunk_tiles;  // this CTA saw all of the keys
+  constexpr int kQuads = HD / 4;
+  auto out_row = [&](int r) {  // row r of this CTA in out, or -1
+    const int rr = rt * R + r, tok = fast_div(rr, a.group_mul, a.group_shift);
+    return tok < seq.n ? (int64_t)(seq.t0 + tok) * a.Hq + kvh * a.group + (rr - tok * a.group) : (int64_t)-1;
+  };
+  if (threadIdx.x < R) {
+    const int r = threadIdx.x;
+    float top = merge_m[r], sum = merge_l[r];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      top = fmaxf(top, merge_m[w * R + r]);
+      sum += merge_l[w * R + r];
+    }
+    cta_ml[r] = make_float2(top, sum);
+    const int64_t row = out_row(r);
+    factor[r] = !whole ? 1.0f : sum == 0.0f ? 0.0f : gs_v / sum;
+    if (!a.cluster && row >= 0) {
+      if (chunk == 0) store_chunks(a, row, tiles);
+      const int64_t at = (int64_t)chunk * a.M * a.Hq + row;
+      if (!whole && FRT_IDX_OK(at, (int64_t)a.M * a.Hq * a.chunks)) a.part_ml[at] = make_float2(top, sum);
+    }
+  }
+  if (!a.cluster) __syncthreads();
+#pragma unroll 4
+  for (int j = 0; j < R * kQuads / kThreads; ++j) {
+    const int i = j * kThreads + threadIdx.x, r = i / kQuads, d = i % kQuads * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float4 u = *reinterpret_cast<const float4*>(merge_o + (size_t)(w * R + r) * A::kOStride + d);
+      const float4 u = *reinterpret_cast<const float4*>(merge_o + (w * R + r) * A::kOStride + d);
       v.x += u.x;
       v.y += u.y;
       v.z += u.z;
       v.w += u.w;
-      sum += merge_l[w * R + r];
     }
-    if (whole) {
-      store_out4(a, row * a.hd + d, v, sum == 0.0f ? 0.0f : gs_v / sum);
+    if (a.cluster) {  // into the place of the first warp's part, which this thread alone reads
+      *reinterpret_cast<float4*>(merge_o + r * A::kOStride + d) = v;
     } else {
-      store_part4(a, chunk, row * a.hd + d, v);
-      const int64_t at = (int64_t)chunk * a.M * a.Hq + row;
-      if (d == 0 && FRT_IDX_OK(at, (int64_t)a.M * a.Hq * a.chunks)) {
-        float top = merge_m[r];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, merge_m[w * R + r]);
-        a.part_ml[at] = make_float2(top, sum);
-      }
+      const int64_t row = out_row(r);
+      if (row < 0 || d >= a.hd) continue;
+      if (whole)
+        store_out4(a, row * a.hd + d, v, factor[r]);
+      else
+        store_part4(a, chunk, row * a.hd + d, v);
     }
   }
+  if (!a.cluster) return;
+  cluster_sync();
+  if (threadIdx.x < R) cluster_factors(a, smem_addr(cta_ml + threadIdx.x), gs_v, factor + threadIdx.x, R);
+  __syncthreads();
+#pragma unroll 1
+  for (int i = chunk * kThreads + threadIdx.x; i < R * kQuads; i += a.chunks * kThreads) {
+    const int r = i / kQuads, d = i % kQuads * 4;
+    const int64_t row = out_row(r);
+    if (row < 0 || d >= a.hd) continue;
+    store_out4(a, row * a.hd + d,
+               join_cluster4(a, smem_addr(merge_o + r * A::kOStride + d), chunk, factor + r, R), 1.0f);
+  }
+  cluster_sync();  // the parts are read
 }
 
-// The chunks' parts of one query row joined: thread groups of hd / 4 lanes take
-// every other chunk, in a fixed order.
+// The chunks' parts of a query row joined, in a fixed order.  TOGETHER: warps of
+// a CTA that share a row (8: one row, many chunks; 1: a row a warp, few).  The
+// loads depend on one another as little as can be: the chunk count and the
+// chunks' maxima are fetched together.
 constexpr int kJoinThreads = 256;
-template <int R>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a, int keys) {
-  __shared__ float4 sums[kJoinThreads];
+constexpr int kJoinWarps = kJoinThreads / 32;
+template <int TOGETHER>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
+  __shared__ float4 sums[TOGETHER > 1 ? kJoinWarps : 1][64];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % TOGETHER;
   const int b = blockIdx.y;
-  int x = blockIdx.x;
-  const int r = x % R;
-  x /= R;
-  const int kvh = x % a.Hkv;
-  const int rt = x / a.Hkv;
+  const int x = blockIdx.x * (kJoinWarps / TOGETHER) + warp / TOGETHER;
+  const int kvh = x % a.Hkv, r = x / a.Hkv;
   pdl_enter();
   const Seq seq = sequence(a, b);
-  const QueryRow mine = query_row(a, seq, rt * R + r, kvh);
-  if (mine.tok < 0) return;
-  const int n = (row_range<R>(a, seq, rt * R, kvh).tiles(keys) + a.chunk_tiles - 1) / a.chunk_tiles;
-  if (n <= 1) return;
-  const int64_t n_rows = (int64_t)a.M * a.Hq, row = (int64_t)mine.tok * a.Hq + mine.head;
+  const int i0 = fast_div(r, a.group_mul, a.group_shift);
+  if (i0 >= seq.n) return;
+  const int64_t n_rows = (int64_t)a.M * a.Hq;
+  const int64_t row = (int64_t)(seq.t0 + i0) * a.Hq + kvh * a.group + (r - i0 * a.group);
   const float kInf = __int_as_float(0x7F800000);
-  const int lane = threadIdx.x & 31;
-  float top = -kInf;
-  for (int i = lane; i < n; i += 32)
+  if (!FRT_IDX_OK(row, n_rows)) return;
+  const float gs_v = __ldg(a.kv_scales + 1);
+  const int n = a.part_n[row];
+  float2 ml = make_float2(-kInf, 0.0f);  // of chunk `lane`; entries behind the count mean nothing
+  if (lane < a.chunks && FRT_IDX_OK(lane * n_rows + row, n_rows * a.chunks)) ml = a.part_ml[lane * n_rows + row];
+  if (n <= 1) return;
+  if (lane >= n) ml = make_float2(-kInf, 0.0f);
+  float top = ml.x;
+  for (int i = 32 + lane; i < n; i += 32)
     if (FRT_IDX_OK(i * n_rows + row, n_rows * a.chunks)) top = fmaxf(top, a.part_ml[i * n_rows + row].x);
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  float sum = 0.0f;
-  for (int i = lane; i < n; i += 32)
-    if (FRT_IDX_OK(i * n_rows + row, n_rows * a.chunks)) {
-      const float2 ml = a.part_ml[i * n_rows + row];
-      sum += ml.y * (ml.x == -kInf ? 0.0f : ex2_approx(ml.x - top));
-    }
-  sum = group_sum<32>(sum);
-
-  const int lanes = a.hd / 4;
-  const int groups = kJoinThreads / lanes;
-  const int grp = threadIdx.x / lanes, d = (threadIdx.x - grp * lanes) * 4;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (grp < groups) {
-#pragma unroll 4
-    for (int i = grp; i < n; i += groups) {
-      const int64_t at = (i * n_rows + row) * a.hd + d;
-      if (!FRT_SPAN_OK(at, 4, n_rows * a.chunks * a.hd)) continue;
-      const float mx = a.part_ml[i * n_rows + row].x;
-      const float f = mx == -kInf ? 0.0f : ex2_approx(mx - top);
-      const float4 u = *reinterpret_cast<const float4*>(a.part_o + at);
-      v.x += u.x * f;
-      v.y += u.y * f;
-      v.z += u.z * f;
-      v.w += u.w * f;
-    }
-  }
-  sums[threadIdx.x] = v;
-  __syncthreads();
-  if (grp != 0) return;
-  for (int i = 1; i < groups; ++i) {
-    const float4 u = sums[i * lanes + threadIdx.x];
-    v.x += u.x;
-    v.y += u.y;
-    v.z += u.z;
-    v.w += u.w;
-  }
-  store_out4(a, row * a.hd + d, v, sum == 0.0f ? 0.0f : __ldg(a.kv_scales + 1) / sum);
-}
-
-// The same with a warp to a row, for many rows and few chunks each.
-constexpr int kJoinRows = kJoinThreads / 32;
-__global__ void __launch_bounds__(kJoinThreads) join_rows_kernel(const Args a, int keys) {
-  static_assert(kTileRows % kJoinRows == 0, "a CTA's rows lie in one row tile");
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  int x = blockIdx.x;
-  const int r = x % (kTileRows / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
-  x /= kTileRows / kJoinRows;
-  const int kvh = x % a.Hkv;
-  const int rt = x / a.Hkv;
-  pdl_enter();
-  const Seq seq = sequence(a, b);
-  const QueryRow mine = query_row(a, seq, rt * kTileRows + r, kvh);
-  const int n = (row_range<kTileRows>(a, seq, rt * kTileRows, kvh).tiles(keys) + a.chunk_tiles - 1) / a.chunk_tiles;
-  if (mine.tok < 0 || n <= 1) return;
-  const int64_t n_rows = (int64_t)a.M * a.Hq, row = (int64_t)mine.tok * a.Hq + mine.head;
-  const float kInf = __int_as_float(0x7F800000);
-  float top = -kInf;
-  for (int i = 0; i < n; ++i)
-    if (FRT_IDX_OK(i * n_rows + row, n_rows * a.chunks)) top = fmaxf(top, a.part_ml[i * n_rows + row].x);
-  float sum = 0.0f;
+  float f = ml.x == -kInf ? 0.0f : ex2_approx(ml.x - top);
+  float sum = ml.y * f;
   float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-  for (int i = 0; i < n; ++i) {
-    if (!FRT_IDX_OK(i * n_rows + row, n_rows * a.chunks)) continue;
-    const float2 ml = a.part_ml[i * n_rows + row];
-    const float f = ml.x == -kInf ? 0.0f : ex2_approx(ml.x - top);
-    sum += ml.y * f;
+  for (int base = 0; base < n; base += 32) {
+    if (base > 0) {
+      ml = make_float2(-kInf, 0.0f);
+      if (base + lane < n && FRT_IDX_OK((base + lane) * n_rows + row, n_rows * a.chunks))
+        ml = a.part_ml[(base + lane) * n_rows + row];
+      f = ml.x == -kInf ? 0.0f : ex2_approx(ml.x - top);
+      sum += ml.y * f;
+    }
+    const int count = min(32, n - base);
+#pragma unroll 4
+    for (int i = part; i < count; i += TOGETHER) {
+      const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
+      const int64_t at0 = ((base + i) * n_rows + row) * a.hd;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int d = 128 * h + 4 * lane;
-      const int64_t at = (i * n_rows + row) * a.hd + d;
-      if (d >= a.hd || !FRT_SPAN_OK(at, 4, n_rows * a.chunks * a.hd)) continue;
-      const float4 u = *reinterpret_cast<const float4*>(a.part_o + at);
-      v[h].x = fmaf(u.x, f, v[h].x);
-      v[h].y = fmaf(u.y, f, v[h].y);
-      v[h].z = fmaf(u.z, f, v[h].z);
-      v[h].w = fmaf(u.w, f, v[h].w);
+      for (int h = 0; h < 2; ++h) {
+        const int d = 128 * h + 4 * lane;
+        if (d >= a.hd || !FRT_SPAN_OK(at0 + d, 4, n_rows * a.chunks * a.hd)) continue;
+        const float4 u = *reinterpret_cast<const float4*>(a.part_o + at0 + d);
+        v[h].x = fmaf(u.x, fi, v[h].x);
+        v[h].y = fmaf(u.y, fi, v[h].y);
+        v[h].z = fmaf(u.z, fi, v[h].z);
+        v[h].w = fmaf(u.w, fi, v[h].w);
+      }
     }
   }
-  const float f = sum == 0.0f ? 0.0f : __ldg(a.kv_scales + 1) / sum;
+  sum = group_sum<32>(sum);
+  if (TOGETHER > 1) {
+    sums[warp][lane] = v[0];
+    sums[warp][32 + lane] = v[1];
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 1; w < TOGETHER; ++w)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 u = sums[warp + w][32 * h + lane];
+        v[h].x += u.x;
+        v[h].y += u.y;
+        v[h].z += u.z;
+        v[h].w += u.w;
+      }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    if (128 * h + 4 * lane < a.hd) store_out4(a, row * a.hd + 128 * h + 4 * lane, v[h], f);
+    if (128 * h + 4 * lane < a.hd) store_out4(a, row * a.hd + 128 * h + 4 * lane, v[h], sum == 0.0f ? 0.0f : gs_v / sum);
 }
 
 // How a call is cut: the rows of a CTA (8 nt, or the tile kernel's), and the
-// keys into chunks of chunk_tiles tiles.
+// keys into chunks.
 struct Plan {
   int nt;  // 0: the tile kernel
-  int row_tiles, chunks, chunk_tiles, keys;
+  int row_tiles, chunks, chunk_tiles, cluster, keys;
 };
-// From this many rows of a sequence and KV head on the tile kernel takes them.
-constexpr int64_t kManyRows = 48;
+// The tile kernel takes calls with at least kManyRows rows to a sequence and KV
+// head and kManyPairs (row, key) pairs times hd / 128: a call of it costs about
+// 10 us and does 1 M such pairs in a microsecond, the kernel for few rows 5 us
+// and 0.27 M.
+constexpr int64_t kManyRows = 48, kManyPairs = 2500000;
 Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
   Plan p;
   const int64_t rows = (int64_t)max_q_len * (Hq / Hkv);
-  p.nt = rows >= kManyRows ? 0 : rows <= 8 ? 1 : rows <= 16 || hd > 128 ? 2 : 4;
+  const double pairs = (double)rows * Hkv * n_seqs * max_kv_len * hd / 128;
+  p.nt = rows >= kManyRows && pairs >= kManyPairs ? 0 : rows <= 8 ? 1 : rows <= 16 || hd > 128 ? 2 : 4;
   const int tile_rows = p.nt == 0 ? kTileRows : 8 * p.nt;
   p.keys = p.nt == 0 ? tile_keys(hd) : kTile;
   const int64_t row_tiles = (rows + tile_rows - 1) / tile_rows;
   p.row_tiles = (int)(row_tiles > 0x7FFFFFFF ? 0x7FFFFFFF : row_tiles);
-  const int64_t tiles = ((int64_t)max_kv_len + 3) / p.keys + 1;
+  const int64_t tiles = max_kv_len > 0 ? ((int64_t)max_kv_len + p.keys - 1) / p.keys : 1;
   const int64_t ctas = row_tiles * Hkv * n_seqs;
-  // enough CTAs for one full wave; a batch of sequences, whose lengths
-  // differ, gets four
-  const int64_t resident = p.nt == 0 ? (hd > 192 ? 1 : 2) : 4;
-  const int64_t want = (int64_t)kSMs * resident * (n_seqs > 1 ? 4 : 1);
-  int64_t chunks = want / (ctas > 0 ? ctas : 1);
-  chunks = chunks < 1 ? 1 : chunks;
-  int64_t per = (tiles + chunks - 1) / chunks;
-  if (p.nt != 0) per = (per + kWarps - 1) / kWarps * kWarps;
-  p.chunk_tiles = (int)per;
-  p.chunks = (int)((tiles + per - 1) / per);
+  // a CTA's smallest share: a tile for every warp
+  const int64_t least = p.nt == 0 ? 1 : kWarps;  // tiles
+  // CTAs that run at once; a batch of sequences, whose lengths differ, gets
+  // four times as many
+  const int64_t want = (int64_t)kSMs * (p.nt == 0 ? (hd > 192 ? 1 : 2) : 4) * (n_seqs > 1 ? 4 : 1);
+  p.cluster = 0;
+  p.chunks = 1;
+  while (p.chunks < 8 && ctas * p.chunks * 2 <= want && tiles > p.chunks * least) p.chunks *= 2;
+  p.chunk_tiles = (int)tiles;
+  if (p.chunks == 1) return p;
+  // More chunks than a cluster has CTAs cost a second kernel and a way through
+  // memory, about as long as kJoinRounds tiles of a warp (or CTA) take.
+  constexpr int64_t kJoinRounds = 8;
+  const int64_t most = want / ctas;
+  int64_t per = (tiles + most - 1) / most;
+  per = (per + least - 1) / least * least;
+  if (tiles / (p.chunks * least) > per / least + kJoinRounds) {
+    p.chunk_tiles = (int)per;
+    p.chunks = (int)((tiles + per - 1) / per);
+  } else {
+    p.cluster = 1;
+  }
   return p;
+}
+
+// floor(p / d) = (p + umulhi(p, mul)) >> shift with 2^shift >= d, mul = floor(2^32
+// (2^shift - d) / d) + 1, for every 0 <= p < 2^31.
+void divisor(int d, uint32_t* mul, int* shift) {
+  *shift = 0;
+  while ((1LL << *shift) < d) ++*shift;
+  *mul = (uint32_t)((((1ULL << *shift) - d) << 32) / d + 1);
 }
 
 bool plan_args_ok(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
@@ -671,8 +698,9 @@ frt_status launch_attn(const Args& a, cudaStream_t stream) {
   static std::atomic<int> opted{48 * 1024};
   const frt_status st = opt_in_smem(attn_kernel<HD, EXACT, NT>, A::kSmem, opted);
   if (st != FRT_OK) return st;
-  return launch(attn_kernel<HD, EXACT, NT>, dim3((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), dim3(kThreads),
-                A::kSmem, stream, a);
+  const dim3 grid((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), block(kThreads);
+  if (a.cluster) return launch_cluster(attn_kernel<HD, EXACT, NT>, grid, block, A::kSmem, stream, a.chunks, a);
+  return launch(attn_kernel<HD, EXACT, NT>, grid, block, A::kSmem, stream, a);
 }
 template <int HD, int NT>
 frt_status launch_exact(const Args& a, cudaStream_t stream) {
@@ -697,8 +725,8 @@ extern "C" size_t frt_attn_nvfp4_workspace_bytes(int M, int n_seqs, int Hq, int 
                                                  int max_kv_len) {
   if (!plan_args_ok(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len)) return 0;
   const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
-  if (p.chunks == 1) return 0;
-  return (size_t)p.chunks * M * Hq * (8 + 4 * (size_t)hd);
+  if (p.chunks == 1 || p.cluster) return 0;
+  return (size_t)M * Hq * (p.chunks * (8 + 4 * (size_t)hd) + 4);
 }
 
 extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_codes, const uint8_t* k_sf,
@@ -739,6 +767,7 @@ extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_cod
   a.out = out;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.chunks * M * Hq * hd);
+  a.part_n = reinterpret_cast<int32_t*>(a.part_ml + (size_t)p.chunks * M * Hq);
   a.status = status;
   a.M = M;
   a.n_seqs = n_seqs;
@@ -755,15 +784,14 @@ extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_cod
     a.page_size = page_size;
     a.max_pages = max_pages;
     a.n_pages = capacity / page_size;
-    // floor(p / d) = (p + umulhi(p, mul)) >> shift with 2^shift >= d,
-    // mul = floor(2^32 (2^shift - d) / d) + 1, for every 0 <= p < 2^31
-    while ((1LL << a.page_shift) < page_size) ++a.page_shift;
-    a.page_mul = (uint32_t)((((1ULL << a.page_shift) - page_size) << 32) / page_size + 1);
+    divisor(page_size, &a.page_mul, &a.page_shift);
   }
+  divisor(a.group, &a.group_mul, &a.group_shift);
   a.window = window;
   a.row_tiles = p.row_tiles;
   a.chunks = p.chunks;
   a.chunk_tiles = p.chunk_tiles;
+  a.cluster = p.cluster;
   a.scale_log2 = softmax_scale * kLog2e;
   a.dt = dt;
   const int rows = p.nt == 0 ? kTileRows : 8 * p.nt;
@@ -772,11 +800,12 @@ extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_cod
                         : p.nt == 1 ? launch_hd<1>(a, stream)
                         : p.nt == 2 ? launch_hd<2>(a, stream)
                                     : launch_hd<4>(a, stream);
-  if (st != FRT_OK || a.chunks == 1) return st;
-  const dim3 grid((unsigned)(Hkv * p.row_tiles * (p.nt == 0 ? rows / kJoinRows : rows)), n_seqs), block(kJoinThreads);
-  return launch(p.nt == 0   ? join_rows_kernel
-                : p.nt == 1 ? join_kernel<8>
-                : p.nt == 2 ? join_kernel<16>
-                            : join_kernel<32>,
-                grid, block, 0, stream, a, p.keys);
+  if (st != FRT_OK || a.chunks == 1 || a.cluster) return st;
+  // rows of a sequence and KV head: no more than max_q_len tokens'
+  const int64_t warps = (int64_t)max_q_len * a.group * Hkv;
+  const bool many = p.chunks > 8;
+  const int64_t gx = many ? warps : (warps + kJoinWarps - 1) / kJoinWarps;
+  if (gx > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
+  return launch(many ? join_kernel<kJoinWarps> : join_kernel<1>, dim3((unsigned)gx, n_seqs), dim3(kJoinThreads), 0,
+                stream, a);
 }

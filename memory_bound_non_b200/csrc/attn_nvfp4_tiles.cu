@@ -29,6 +29,7 @@ namespace frt {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr size_t kSmallBytes = 9 * 1024;     // struct Small
 constexpr int kQRegion = kTileRows * 128;  // bytes of 64 dimensions of all rows
 
 template <int HD>
@@ -39,7 +40,9 @@ struct Tile {
   static constexpr int U = KT * C / 64;      // 16-element blocks a thread converts
   static constexpr int kCols = KT + HD <= 256 ? 256 : 512;  // TMEM columns: S (P over it), O
   static constexpr int kO = KT;                             // first column of O
-  static constexpr size_t kSmem = 1024 + C * (kQRegion + 2 * kRegion) + 4096;
+  // (a cluster's parts, 128 rows of HD floats, fit over the operands)
+  static_assert(kTileRows * HD * 4 <= C * (kQRegion + 2 * kRegion), "parts over the operands");
+  static constexpr size_t kSmem = 1024 + C * (kQRegion + 2 * kRegion) + kSmallBytes;
 };
 
 // ------------------------------------------------------------ tcgen05 --
@@ -120,6 +123,34 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+__device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+// x plus both halves of w, one rounding each.
+__device__ __forceinline__ float add_halves(float x, uint32_t w) {
+  asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
+      "add.rn.f32.f16 %0, lo, %0;\n\tadd.rn.f32.f16 %0, hi, %0;\n\t}"
+      : "+f"(x)
+      : "r"(w));
+  return x;
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy_async16(uint32_t to, const void* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
 struct Small {  // behind the operands
   float top[2][kTileRows];    // each half's largest score of a row; at the end its sum
   float scale[kTileRows];     // score -> log2 units
@@ -127,11 +158,13 @@ struct Small {  // behind the operands
   int slot[2][32];            // quad slots of a tile, by tile parity
   int holes[2];               // a tile has quads that are not there
   uint32_t nan[4];            // keys of the tile with a NaN factor in V
+  float2 ml[kTileRows];       // (maximum, sum) of a row, for the cluster
+  float factor[8][kTileRows];
   uint64_t s_done, o_done;
   uint32_t tmem;
   int gave_up;
 };
-static_assert(sizeof(Small) <= 4096, "fits behind the operands");
+static_assert(sizeof(Small) <= kSmallBytes, "fits behind the operands");
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const AttnArgs a, int polls) {
@@ -144,20 +177,17 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.y;
-  int x = blockIdx.x;
-  const int kvh = x % a.Hkv;
-  x /= a.Hkv;
-  const int rt = x % a.row_tiles;
-  const int chunk = x / a.row_tiles;
+  const Place place = place_of(a);
+  const int kvh = place.kvh, rt = place.rt, chunk = place.chunk;
 
   pdl_enter();
   const Seq seq = sequence(a, b);
   const RowRange range = row_range<kTileRows>(a, seq, rt * kTileRows, kvh);
   if (range.bad && a.status != nullptr) atomicOr(a.status, 1);
   const int tiles = range.tiles(KT);
-  const int tile0 = chunk * a.chunk_tiles;
-  if (!range.any || (chunk > 0 && tile0 >= tiles)) return;  // no rows, or no work
-  const int tile1 = min(tile0 + a.chunk_tiles, tiles);
+  const int2 part = tiles_of(a, chunk, tiles);
+  const int tile0 = part.x, tile1 = part.y;
+  if (!range.any || (!a.cluster && chunk > 0 && tile0 >= tiles)) return;  // no rows, or no work
 
   // this thread's row and half of the columns (TMEM lanes are split by warp % 4)
   const int row = 32 * (warp & 3) + lane, half = warp >> 2;
@@ -191,38 +221,45 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
   const uint32_t tmem = sm.tmem;
   const uint32_t s_tmem = tmem + ((uint32_t)(warp & 3) << 21), o_tmem = s_tmem + T::kO;
 
-  // The blocks that this thread converts: of unit i key key_of(i), region
-  // kc_of(i), block 4 kc + lane % 4.
-  auto kc_of = [&](int i) { return (warp * 4 + (lane >> 3) + 32 * i) % C; };
-  auto key_of = [&](int i) { return 2 * ((warp * 4 + (lane >> 3) + 32 * i) / C) + ((lane >> 2) & 1); };
+  // The blocks that this thread converts: of unit i key key0 + 64 (i / C), region
+  // i % C, block lane % 4 of it.
+  const int key0 = 8 * warp + 2 * (lane >> 3) + ((lane >> 2) & 1);
   struct Raw {
     uint2 c[U];
     uint32_t sf[U];
   };
-  const int row_bytes = a.Hkv * (a.hd >> 1);
+  const int row_bytes = a.Hkv * (a.hd >> 1), sf_row = a.Hkv * nblk;
+  const int code0 = (key0 & 3) * row_bytes + kvh * (a.hd >> 1) + 8 * (lane & 3);
+  const int sf0 = (kvh * nblk + (lane & 3)) * 4 + (key0 & 3);
   auto load = [&](const uint8_t* codes, const uint8_t* sf, int tile, Raw& r) {
-    const int left = range.all_hi - (range.first() + tile * KT);
+    const int left = range.all_hi - (range.first() + tile * KT) - key0;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int key = key_of(i), blk = 4 * kc_of(i) + (lane & 3);
-      const int quad = tile < tile1 ? sm.slot[tile & 1][key >> 2] : -1;
-      r.c[i] = make_uint2(0, 0);
-      r.sf[i] = 0;
-      if (quad >= 0 && key < left && blk < nblk) {
-        const int64_t at = (int64_t)(quad + (key & 3)) * row_bytes + kvh * (a.hd >> 1) + 8 * blk;
-        const int64_t s = (int64_t)quad * (a.Hkv * nblk) + (kvh * nblk + blk) * 4 + (key & 3);
-        if (FRT_SPAN_OK(at, 8, (int64_t)a.capacity * row_bytes))
-          r.c[i] = ld_stream(reinterpret_cast<const uint2*>(codes + at));
-        if (FRT_IDX_OK(s, (int64_t)((a.capacity + 3) >> 2) * a.Hkv * nblk * 4)) r.sf[i] = __ldg(sf + s);
+    for (int j = 0; j < U / C; ++j) {
+      const int quad = tile < tile1 ? sm.slot[tile & 1][(key0 >> 2) + 16 * j] : -1;
+      const bool on = quad >= 0 && 64 * j < left;
+      const uint8_t* pc = codes + code0 + (int64_t)quad * row_bytes;
+      const uint8_t* ps = sf + sf0 + (int64_t)quad * sf_row;
+#pragma unroll
+      for (int kc = 0; kc < C; ++kc) {
+        const int i = j * C + kc;
+        r.c[i] = make_uint2(0, 0);
+        r.sf[i] = 0;
+        if (on && 4 * kc + (lane & 3) < nblk) {
+          if (FRT_SPAN_OK(pc + 32 * kc - codes, 8, (int64_t)a.capacity * row_bytes))
+            r.c[i] = ld_stream(reinterpret_cast<const uint2*>(pc + 32 * kc));
+          if (FRT_IDX_OK(ps + 16 * kc - sf, (int64_t)((a.capacity + 3) >> 2) * sf_row * 4)) r.sf[i] = __ldg(ps + 16 * kc);
+        }
       }
     }
   };
+  const int line0 = key0 * 128 + (((2 * (lane & 3)) ^ (key0 & 7)) << 4);
+  const int line1 = key0 * 128 + (((2 * (lane & 3) + 1) ^ (key0 & 7)) << 4);
   auto convert = [&](const Raw& r, uint32_t to, bool is_v) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int key = key_of(i);
       uint32_t sf = r.sf[i];
       if (is_v && (sf & 0x7F) == 0x7F) {
+        const int key = key0 + 64 * (i / C);
         sf = 0;
         atomicOr(&sm.nan[key >> 5], 1u << (key & 31));
       }
@@ -232,10 +269,9 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
       e2m1x8_to_half2(r.c[i].y, h + 4);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = hmul2(h[e], f[0]);
-      const uint32_t line = to + kc_of(i) * kRegion + key * 128;
-      const int piece = 2 * (lane & 3);
-      st_shared16(line + ((piece ^ (key & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
-      st_shared16(line + (((piece + 1) ^ (key & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+      const uint32_t at = to + (i % C) * kRegion + (i / C) * 64 * 128;
+      st_shared16(at + line0, make_uint4(h[0], h[1], h[2], h[3]));
+      st_shared16(at + line1, make_uint4(h[4], h[5], h[6], h[7]));
     }
   };
   bool gave_up = false;
@@ -255,25 +291,36 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
     const float c = a.scale_log2 * __ldg(a.kv_scales);
     const uint32_t flip = c < 0.0f ? 0x80008000u : 0u;
     const int l = lane % kLanes;
-#pragma unroll 4
-    for (int i = 0; i < kTileRows / (8 * kRows); ++i) {
-      const int r = (i * 8 + warp) * kRows + lane / kLanes;
-      const int tok = sm.tok[r];
-      uint4 v = make_uint4(0, 0, 0, 0);
-      const int64_t at = ((int64_t)tok * a.Hq + sm.head[r]) * (a.hd / 8) + l;
-      if (tok >= 0 && l < a.hd / 8 && FRT_IDX_OK(at, (int64_t)a.M * a.Hq * (a.hd / 8)))
-        v = ld_plain(static_cast<const uint4*>(a.q) + at);
+    // Copied as they are to where they belong, then converted there: short
+    // loops, since code that runs once costs its instruction fetches.
+    auto q_row = [&](int i) { return (i * 8 + warp) * kRows + lane / kLanes; };
+    auto q_at = [&](int r) { return q_smem + (l >> 3) * kQRegion + r * 128 + (((l & 7) ^ (r & 7)) << 4); };
+    constexpr int kIters = kTileRows / (8 * kRows);
+#pragma unroll 2
+    for (int i = 0; i < kIters; ++i) {
+      const int r = q_row(i), tok = sm.tok[r];
+      const int64_t at = ((int64_t)max(tok, 0) * a.Hq + sm.head[r]) * (a.hd / 8) + min(l, a.hd / 8 - 1);
+      const bool on = tok >= 0 && l < a.hd / 8 && FRT_IDX_OK(at, (int64_t)a.M * a.Hq * (a.hd / 8));
+      if (l < HD / 8) copy_async16(q_at(r), static_cast<const uint4*>(a.q) + at, on);
+    }
+    copy_async_wait();
+#pragma unroll 1
+    for (int i = 0; i < kIters; ++i) {
+      const int r = q_row(i);
       float s = 1.0f;
-      if (a.dt == FRT_BF16) {
-        float2 f[4];
-        unpack_pairs<FRT_BF16, 4>(&v.x, f);
-        const float amax = fmaxf(absmax4(f[0].x, f[0].y, f[1].x, f[1].y), absmax4(f[2].x, f[2].y, f[3].x, f[3].y));
-        s = pow2_to_half_range(kLanes == 16 ? half_warp_max_abs(amax) : warp_max_abs(amax));
-        mul_pairs<4>(f, s);
-        pack_pairs<FRT_F16, 4>(f, &v.x);
+      if (a.dt == FRT_BF16 || flip != 0) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (l < HD / 8) v = ld_shared16(q_at(r));
+        if (a.dt == FRT_BF16) {
+          float2 f[4];
+          unpack_pairs<FRT_BF16, 4>(&v.x, f);
+          const float amax = fmaxf(absmax4(f[0].x, f[0].y, f[1].x, f[1].y), absmax4(f[2].x, f[2].y, f[3].x, f[3].y));
+          s = pow2_to_half_range(kLanes == 16 ? half_warp_max_abs(amax) : warp_max_abs(amax));
+          mul_pairs<4>(f, s);
+          pack_pairs<FRT_F16, 4>(f, &v.x);
+        }
+        if (l < HD / 8) st_shared16(q_at(r), make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
       }
-      v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
-      if (l < HD / 8) st_shared16(q_smem + (l >> 3) * kQRegion + r * 128 + (((l & 7) ^ (r & 7)) << 4), v);
       // (never 0, which would make a masked score NaN)
       if (l == 0) sm.scale[r] = fmaxf(fabsf(c) / s, 0x1p-120f);
     }
@@ -367,8 +414,7 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
     for (int i = 0; i < KT / 4; ++i) {
       p[i] = Pack16<FRT_F16>::from_float2(ex2_approx(fmaf(__uint_as_float(s[2 * i]), c, shift)),
                                           ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), c, shift)));
-      const float2 u = Pack16<FRT_F16>::to_float2(p[i]);
-      sum += u.x + u.y;
+      sum = add_halves(sum, p[i]);
     }
     if constexpr (KT == 128)
       tc_st32(s_tmem + half * 32, p);
@@ -396,9 +442,12 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
   __syncthreads();
   tc_fence_after();
   sum += sm.top[half ^ 1][row];
-  const bool whole = tiles <= a.chunk_tiles;  // this CTA saw all of the keys
-  const float f = !whole ? 1.0f : sum == 0.0f ? 0.0f : __ldg(a.kv_scales + 1) / sum;
-  const int64_t q_row = (int64_t)mine.tok * a.Hq + mine.head;
+  const bool whole = !a.cluster && tiles <= a.chunk_tiles;  // this CTA saw all of the keys
+  const float gs_v = __ldg(a.kv_scales + 1);
+  // The sums go through shared memory, over the operands that nothing reads any
+  // more (128 rows of HD floats, their 16-byte pieces swizzled by row), so that
+  // neighbouring threads write neighbouring dimensions and the CTAs of a cluster
+  // can read one another's.
 #pragma unroll 1
   for (int i = 0; i < HD / 64; ++i) {
     uint32_t o[32];
@@ -411,21 +460,57 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
       for (int e = 0; e < 32; ++e) o[e] = 0;
     }
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      if (mine.tok < 0 || d0 + e >= a.hd) continue;
-      const float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                   __uint_as_float(o[e + 3]));
-      if (whole)
-        store_out4(a, q_row * a.hd + d0 + e, v, f);
-      else
-        store_part4(a, chunk, q_row * a.hd + d0 + e, v);
+    for (int e = 0; e < 32; e += 4)
+      st_shared16(base + row * (HD * 4) + ((((d0 + e) >> 2) ^ (row & 7)) << 4),
+                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+  }
+  if (half == 0) {
+    sm.ml[row] = make_float2(m, sum);
+    if (!a.cluster && mine.tok >= 0) {
+      const int64_t q_row = (int64_t)mine.tok * a.Hq + mine.head;
+      if (chunk == 0) store_chunks(a, q_row, tiles);
+      const int64_t at = (int64_t)chunk * a.M * a.Hq + q_row;
+      if (!whole && FRT_IDX_OK(at, (int64_t)a.M * a.Hq * a.chunks)) a.part_ml[at] = make_float2(m, sum);
     }
-    __syncwarp();
   }
-  if (!whole && mine.tok >= 0 && half == 0) {
-    const int64_t at = (int64_t)chunk * a.M * a.Hq + q_row;
-    if (FRT_IDX_OK(at, (int64_t)a.M * a.Hq * a.chunks)) a.part_ml[at] = make_float2(m, sum);
+  if (a.cluster)
+    cluster_sync();
+  else
+    __syncthreads();
+  // each row's factors for the parts
+  const int ctas = a.cluster ? a.chunks : 1, rank = a.cluster ? chunk : 0;
+  if (threadIdx.x < kTileRows) {
+    const int r = threadIdx.x;
+    if (a.cluster) {
+      cluster_factors(a, smem_addr(sm.ml + r), gs_v, &sm.factor[0][r], kTileRows);
+    } else {
+      const float total = sm.ml[r].y;
+      sm.factor[0][r] = !whole ? 1.0f : total == 0.0f ? 0.0f : gs_v / total;
+    }
   }
+  __syncthreads();
+  // pieces of four dimensions, dealt to the CTAs of a cluster
+#pragma unroll 1
+  for (int i = rank * kThreads + threadIdx.x; i < kTileRows * (HD / 4); i += ctas * kThreads) {
+    const int r = i / (HD / 4), d = i % (HD / 4) * 4;
+    const int tok = sm.tok[r];
+    if (tok < 0 || d >= a.hd) continue;
+    const int64_t at = ((int64_t)tok * a.Hq + sm.head[r]) * a.hd + d;
+    const uint32_t piece = base + r * (HD * 4) + (((d >> 2) ^ (r & 7)) << 4);
+    float4 v;
+    if (a.cluster) {
+      v = join_cluster4(a, piece, rank, &sm.factor[0][r], kTileRows);
+    } else {
+      const float4 u = ld_shared4(piece);
+      const float f = sm.factor[0][r];
+      v = make_float4(u.x * f, u.y * f, u.z * f, u.w * f);
+    }
+    if (a.cluster || whole)
+      store_out4(a, at, v, 1.0f);
+    else
+      store_part4(a, chunk, at, v);
+  }
+  if (a.cluster) cluster_sync();  // the parts are read
   // a wait that ran out: report it, and let the products end before TMEM is freed
   if (sm.gave_up != 0 && threadIdx.x == 0) {
     if (a.status != nullptr) atomicOr(a.status, 2);
@@ -442,8 +527,10 @@ frt_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
   static std::atomic<int> opted{48 * 1024};
   const frt_status st = opt_in_smem(tiles_kernel<HD>, Tile<HD>::kSmem, opted);
   if (st != FRT_OK) return st;
-  return launch(tiles_kernel<HD>, dim3((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), dim3(kThreads),
-                Tile<HD>::kSmem, stream, a, wait_polls());
+  const dim3 grid((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), block(kThreads);
+  if (a.cluster)
+    return launch_cluster(tiles_kernel<HD>, grid, block, Tile<HD>::kSmem, stream, a.chunks, a, wait_polls());
+  return launch(tiles_kernel<HD>, grid, block, Tile<HD>::kSmem, stream, a, wait_polls());
 }
 
 }  // namespace
