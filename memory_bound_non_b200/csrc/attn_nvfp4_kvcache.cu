@@ -34,8 +34,6 @@
 namespace frt {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;  // slots
 constexpr int kSMs = 148;
 using Args = AttnArgs;
@@ -44,18 +42,53 @@ __device__ __forceinline__ uint32_t select_bits(uint32_t mask, uint32_t a, uint3
   return (a & mask) | (b & ~mask);
 }
 
+// Warps of a CTA: eight where registers let two such CTAs share an SM.
+__host__ __device__ constexpr int attn_warps(int hd_build, int nt) { return nt == 1 && hd_build == 128 ? 8 : 4; }
+
+// BYTES to shared memory, or zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool on) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(BYTES), "r"(on ? BYTES : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // HD: head dimension of the build (a multiple of 64, at least hd); EXACT: hd ==
 // HD; NT: query rows / 8.
+//
+// A warp's tiles come through its own ring of kStages tiles in shared memory
+// (K codes, V codes, their factors), kStages - 1 of them on their way: 9 KB a
+// warp at HD 128, what the HBM latency asks for, and none of it in registers.
+// Rows are stored so that the lanes' reads are free of bank conflicts: K's
+// slots 4g + i at (i, g), V's 8t + i at (i, t) with the upper 16 slots' 32-byte
+// halves swapped.
 template <int HD, bool EXACT, int NT>
 struct Attn {
   static constexpr int J = HD / 64;
   static constexpr int R = 8 * NT;
+  static constexpr int W = attn_warps(HD, NT);
+  static constexpr int kThreads = 32 * W;
   static constexpr int kSteps = HD / 16;
   static constexpr int kVs = J == 3 ? 3 : (J + 1) / 2;  // factor words a lane and quad of V
+  static constexpr int kStages = HD == 256 ? 2 : 3;
+  static constexpr int kRow = HD / 2;          // bytes of a slot's codes
+  static constexpr int kSfRow = HD / 4;        // bytes of a quad's factors
+  static constexpr int kV = kTile * kRow, kKSf = 2 * kV, kVSf = kKSf + 8 * kSfRow, kStage = kVSf + 8 * kSfRow;
+  static constexpr int kMinCtas =
+      W == 8 ? 2 : HD / 64 * NT <= 2 ? 4 : HD / 64 * NT <= 4 && HD <= 128 ? 3 : 2;
   static constexpr int kOStride = HD + 4;
-  static constexpr size_t kQBytes = (size_t)kSteps * NT * 32 * 8;
-  static constexpr size_t kMergeBytes = (size_t)kWarps * R * kOStride * 4;
-  static constexpr size_t kSmem = (kQBytes > kMergeBytes ? kQBytes : kMergeBytes) + R * 4 + 2 * kWarps * R * 4 + R * 8 + 8 * R * 4;
+  static constexpr size_t kRing = (size_t)W * kStages * kStage;
+  static constexpr size_t kMerge = (size_t)W * R * kOStride * 4;
+  static constexpr size_t kQ = kRing > kMerge ? kRing : kMerge;  // the merged parts lie over the ring
+  static constexpr size_t kSmall = kQ + (size_t)kSteps * NT * 32 * 8;
+  static constexpr size_t kSmem = kSmall + R * 4 + 2 * W * R * 4 + R * 8 + 8 * R * 4;
 
   struct KFrag {
     uint32_t c[4][2 * J];
@@ -66,139 +99,129 @@ struct Attn {
     uint32_t sf[2][kVs];
   };
 
-  // Where this lane's part of slot 0 lies; a slot's codes are row_bytes on, and
-  // the factors of the quad that begins with slot s are s * sf_row on.  Blocks
-  // behind hd (a build of a larger HD) are the last one again; K's factors are
-  // cleared there (k_keep), V's dimensions are not written.
-  struct Base {
-    const uint8_t* k;
-    const uint8_t* v;
-    const uint8_t* k_sf;
-    const uint8_t* v_sf;
-    int row_bytes, sf_row, last;
-    int k_off[J], v_off[J], v_sf_off[kVs];
-    uint32_t k_keep[J];
-    __device__ __forceinline__ Base(const Args& a, int kvh, int g, int t) {
-      const int nblk = a.hd >> 4;
-      k = a.k_codes + kvh * (a.hd >> 1);
-      v = a.v_codes + kvh * (a.hd >> 1);
-      k_sf = a.k_sf + kvh * nblk * 4;
-      v_sf = a.v_sf + kvh * nblk * 4;
-      row_bytes = a.Hkv * (a.hd >> 1);
-      sf_row = a.Hkv * nblk;
-      last = a.capacity - 1;
+  static __device__ __forceinline__ int k_at(int row) { return ((row & 3) * 8 + (row >> 2)) * kRow; }
+  static __device__ __forceinline__ int v_at(int row) { return kV + ((row & 7) * 4 + (row >> 3)) * kRow; }
+  static __device__ __forceinline__ int v_swap(int row) { return J == 2 ? (row >> 4 & 1) * 32 : 0; }
+
+  // Starts the copies of a tile: `slot` is the first slot of the lane's quad g
+  // (-1: not there), `left` the positions from the tile's first to the end.
+  static __device__ __forceinline__ void fetch(const Args& a, int kvh, int slot, int left, int lane, uint32_t to) {
+    const int nblk = a.hd >> 4;
+    const int row_bytes = a.Hkv * (a.hd >> 1), sf_row = a.Hkv * nblk;
+    const uint8_t* k = a.k_codes + kvh * (a.hd >> 1);
+    const uint8_t* v = a.v_codes + kvh * (a.hd >> 1);
+    const uint8_t* k_sf = a.k_sf + kvh * nblk * 4;
+    const uint8_t* v_sf = a.v_sf + kvh * nblk * 4;
+    const int64_t code_bytes = (int64_t)a.capacity * row_bytes;
+    const int64_t sf_bytes = (int64_t)((a.capacity + 3) >> 2) * sf_row * 4;
+    if constexpr (EXACT) {
+      constexpr int kPieces = kRow / 16;  // of a row
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int row = (32 * i + lane) / kPieces, piece = (32 * i + lane) % kPieces * 16;
+        const int quad = __shfl_sync(0xFFFFFFFFu, slot, row & ~3);  // lane 4 (row / 4)
+        bool on = quad >= 0 && row < left;
+        const int64_t at = (int64_t)(on ? quad + (row & 3) : 0) * row_bytes + piece;
+        on = on && FRT_SPAN_OK(k + at - a.k_codes, 16, code_bytes);
+        copy_async<16>(to + k_at(row) + piece, k + at, on);
+        copy_async<16>(to + v_at(row) + (piece ^ v_swap(row)), v + at, on);
+      }
+      constexpr int kSfPieces = kSfRow / 16, kHalf = 8 * kSfPieces;
+#pragma unroll
+      for (int i = 0; i < (2 * kHalf + 31) / 32; ++i) {
+        const int id = 32 * i + lane, q = id % kHalf / kSfPieces, piece = id % kSfPieces * 16;
+        const int quad = __shfl_sync(0xFFFFFFFFu, slot, 4 * q);
+        const uint8_t* from = (id < kHalf ? k_sf : v_sf) + (int64_t)max(quad, 0) * sf_row + piece;
+        const bool on = quad >= 0 && FRT_SPAN_OK(from - (id < kHalf ? a.k_sf : a.v_sf), 16, sf_bytes);
+        if (2 * kHalf % 32 == 0 || id < 2 * kHalf)
+          copy_async<16>(to + (id < kHalf ? kKSf : kVSf) + q * kSfRow + piece, from, on);
+      }
+    } else {  // rows of any multiple of 8 bytes: a lane a row
+      const int quad = __shfl_sync(0xFFFFFFFFu, slot, lane & ~3);
+      bool on = quad >= 0 && lane < left;
+      const int64_t at = (int64_t)(on ? quad + (lane & 3) : 0) * row_bytes;
+      on = on && FRT_SPAN_OK(k + at - a.k_codes, a.hd >> 1, code_bytes);
+      for (int c = 0; c < nblk; ++c) {
+        copy_async<8>(to + k_at(lane) + 8 * c, k + at + 8 * c, on);
+        copy_async<8>(to + v_at(lane) + (8 * c ^ v_swap(lane)), v + at + 8 * c, on);
+      }
+      for (int c = lane & 3; c < nblk; c += 4) {
+        const int64_t s = (int64_t)max(slot, 0) * sf_row + 4 * c;
+        const bool there = slot >= 0 && FRT_SPAN_OK(k_sf + s - a.k_sf, 4, sf_bytes);
+        copy_async<4>(to + kKSf + (lane >> 2) * kSfRow + 4 * c, k_sf + s, there);
+        copy_async<4>(to + kVSf + (lane >> 2) * kSfRow + 4 * c, v_sf + s, there);
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void read_k(const unsigned char* stage, int g, int t, KFrag& f) {
+    const unsigned char* p = stage + g * kRow + 8 * J * t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        k_off[j] = EXACT ? t * J + j : min(t * J + j, nblk - 1);
-        k_keep[j] = EXACT || t * J + j < nblk ? 0xFFFFFFFFu : 0u;
-        v_off[j] = EXACT ? g * J + j : min(g * J + j, 2 * nblk - 1);
-      }
-#pragma unroll
-      for (int j = 0; j < kVs; ++j) v_sf_off[j] = v_off[J == 3 ? j : 2 * j] >> 1;
-    }
-  };
-  static __device__ __forceinline__ bool code_ok(const Args& a, const uint8_t* p, const uint8_t* base, int bytes) {
-    return FRT_SPAN_OK(p - base, bytes, (int64_t)a.capacity * a.Hkv * (a.hd >> 1));
-  }
-  static __device__ __forceinline__ bool sf_ok(const Args& a, const uint8_t* p, const uint8_t* base) {
-    return FRT_SPAN_OK(p - base, 4, (int64_t)((a.capacity + 3) >> 2) * a.Hkv * (a.hd >> 4) * 4);
-  }
-
-  // The four slots from `slot` on.  Every load is made: a quad that is not
-  // there (slot < 0) is slot 0, slots behind the capacity are the last one;
-  // what they bring is masked by position later.
-  static __device__ __forceinline__ void load_k(const Args& a, const Base& base, int slot, KFrag& f) {
-    const int s0 = max(slot, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* p = base.k + (int64_t)min(s0 + i, base.last) * base.row_bytes;
-      if (EXACT && (J & 1) == 0) {
-        p += 8 * base.k_off[0];
-#pragma unroll
-        for (int j = 0; j < J; j += 2) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (code_ok(a, p + 8 * j, a.k_codes, 16)) v = ld_stream(reinterpret_cast<const uint4*>(p + 8 * j));
-          f.c[i][2 * j] = v.x;
-          f.c[i][2 * j + 1] = v.y;
-          f.c[i][2 * j + 2] = v.z;
-          f.c[i][2 * j + 3] = v.w;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const uint8_t* pj = p + (EXACT ? 8 * base.k_off[0] + 8 * j : 8 * base.k_off[j]);
-          uint2 v = make_uint2(0, 0);
-          if (code_ok(a, pj, a.k_codes, 8)) v = ld_stream(reinterpret_cast<const uint2*>(pj));
+        const unsigned char* q = p + i * 8 * kRow + 8 * j;
+        if (J % 2 == 0) {
+          if (j % 2 == 0) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q);
+            f.c[i][2 * j] = v.x;
+            f.c[i][2 * j + 1] = v.y;
+            f.c[i][(2 * j + 2) % (2 * J)] = v.z;
+            f.c[i][(2 * j + 3) % (2 * J)] = v.w;
+          }
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(q);
           f.c[i][2 * j] = v.x;
           f.c[i][2 * j + 1] = v.y;
         }
       }
-    }
-    const uint8_t* s = base.k_sf + (int64_t)s0 * base.sf_row;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint8_t* sj = s + (EXACT ? 4 * base.k_off[0] + 4 * j : 4 * base.k_off[j]);
-      f.sf[j] = 0;
-      if (sf_ok(a, sj, a.k_sf)) f.sf[j] = __ldg(reinterpret_cast<const uint32_t*>(sj));
-    }
+    for (int j = 0; j < J; ++j)
+      f.sf[j] = *reinterpret_cast<const uint32_t*>(stage + kKSf + g * kSfRow + 4 * (J * t + j));
   }
-
-  // Half h of a lane's slots: the quad from `slot` on, as load_k.
-  static __device__ __forceinline__ void load_v(const Args& a, const Base& base, int h, int slot, VFrag& f) {
-    const int s0 = max(slot, 0);
+  static __device__ __forceinline__ void read_v(const unsigned char* stage, int g, int t, VFrag& f) {
+    const unsigned char* p = stage + kV + t * kRow + (4 * J * g ^ (J == 2 ? (t >> 1) * 32 : 0));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* p = base.v + (int64_t)min(s0 + i, base.last) * base.row_bytes;
-      if (J == 4 && EXACT) {
-        p += 4 * base.v_off[0];
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (code_ok(a, p, a.v_codes, 16)) v = ld_stream(reinterpret_cast<const uint4*>(p));
-        f.c[h][i][0] = v.x;
-        f.c[h][i][1 % J] = v.y;
-        f.c[h][i][2 % J] = v.z;
-        f.c[h][i][3 % J] = v.w;
-      } else if ((J & 1) == 0) {
-        // (hd / 8 is even, so a clamped pair begins at hd / 8 - 2)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < J; j += 2) {
-          const uint8_t* pj = p + (EXACT ? 4 * base.v_off[0] + 4 * j : 4 * (base.v_off[j] & ~1));
-          uint2 v = make_uint2(0, 0);
-          if (code_ok(a, pj, a.v_codes, 8)) v = ld_stream(reinterpret_cast<const uint2*>(pj));
-          f.c[h][i][j] = v.x;
-          f.c[h][i][(j + 1) % J] = v.y;
-        }
-      } else {
+      for (int i = 0; i < 4; ++i) {
+        const unsigned char* q = p + (4 * h + i) * 4 * kRow;
+        if (J == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(q);
+          f.c[h][i][0] = v.x;
+          f.c[h][i][1 % J] = v.y;
+          f.c[h][i][2 % J] = v.z;
+          f.c[h][i][3 % J] = v.w;
+        } else if (J == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(q);
+          f.c[h][i][0] = v.x;
+          f.c[h][i][1 % J] = v.y;
+        } else {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const uint8_t* pj = p + (EXACT ? 4 * base.v_off[0] + 4 * j : 4 * base.v_off[j]);
-          f.c[h][i][j] = 0;
-          if (code_ok(a, pj, a.v_codes, 4)) f.c[h][i][j] = __ldg(reinterpret_cast<const uint32_t*>(pj));
+          for (int j = 0; j < J; ++j) f.c[h][i][j] = *reinterpret_cast<const uint32_t*>(q + 4 * j);
         }
       }
-    }
-    const uint8_t* s = base.v_sf + (int64_t)s0 * base.sf_row;
+  }
+  static __device__ __forceinline__ void read_v_sf(const unsigned char* stage, int g, int t, VFrag& f) {
 #pragma unroll
-    for (int j = 0; j < kVs; ++j) {
-      const uint8_t* sj = s + 4 * base.v_sf_off[j];
-      f.sf[h][j] = 0;
-      if (sf_ok(a, sj, a.v_sf)) f.sf[h][j] = __ldg(reinterpret_cast<const uint32_t*>(sj));
-    }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < kVs; ++j) {
+        const int blk = (g * J + (J == 3 ? j : 2 * j)) >> 1;
+        f.sf[h][j] = *reinterpret_cast<const uint32_t*>(stage + kVSf + (2 * t + h) * kSfRow + 4 * blk);
+      }
   }
 };
 
 template <int HD, bool EXACT, int NT>
-__host__ __device__ constexpr int min_ctas() {
-  return HD / 64 * NT <= 2 ? 4 : HD / 64 * NT <= 4 && HD <= 128 ? 3 : 2;
-}
-
-template <int HD, bool EXACT, int NT>
-__global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kernel(const Args a) {
+__global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT, NT>::kMinCtas)
+    attn_kernel(const Args a) {
   using A = Attn<HD, EXACT, NT>;
-  constexpr int J = A::J, R = A::R;
+  constexpr int J = A::J, R = A::R, kWarps = A::W, kThreads = A::kThreads, kStages = A::kStages;
   extern __shared__ __align__(16) unsigned char smem[];
-  uint2* q_frag = reinterpret_cast<uint2*>(smem);
+  uint2* q_frag = reinterpret_cast<uint2*>(smem + A::kQ);
   float* merge_o = reinterpret_cast<float*>(smem);
-  float* q_scale = reinterpret_cast<float*>(smem + A::kSmem - R * 4 - 2 * kWarps * R * 4 - R * 8 - 8 * R * 4);
+  float* q_scale = reinterpret_cast<float*>(smem + A::kSmall);
   float* merge_m = q_scale + R;
   float* merge_l = merge_m + kWarps * R;
   float2* cta_ml = reinterpret_cast<float2*>(merge_l + kWarps * R);
@@ -223,24 +246,30 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
   const float gs_k = __ldg(a.kv_scales), gs_v = __ldg(a.kv_scales + 1);
 
   // first loads, on their way while the queries are laid out
-  const typename A::Base base(a, kvh, g, t);
-  typename A::KFrag kf;
-  typename A::VFrag vf;
+  unsigned char* ring = smem + warp * kStages * A::kStage;
   int tile = tile0 + warp;
   auto position = [&](int tl) { return rows.first() + tl * kTile + 4 * g; };
   auto slot_of = [&](int tl) { return tl < tile1 ? quad_slot(a, b, position(tl), rows) : -1; };
-  auto fetch_k = [&](int slot) { A::load_k(a, base, slot, kf); };
-  auto fetch_v = [&](int slot) {
-    A::load_v(a, base, 0, __shfl_sync(0xFFFFFFFFu, slot, 8 * t), vf);
-    A::load_v(a, base, 1, __shfl_sync(0xFFFFFFFFu, slot, 8 * t + 4), vf);
+  auto fetch = [&](int tl, int slot, int stage) {
+    if (tl < tile1)
+      A::fetch(a, kvh, slot, rows.all_hi - (rows.first() + tl * kTile), lane, smem_addr(ring + stage * A::kStage));
+    copy_async_commit();
   };
-  int slot = slot_of(tile);
-  int slot_next = slot_of(tile + kWarps);
-  fetch_k(slot);
-  fetch_v(slot);
+  if (!EXACT) {  // factors of blocks behind hd stay 0
+    for (int i = lane; i < kStages * 4 * HD / 4; i += 32) {
+      const int stage = i / HD, w = i % HD;
+      *reinterpret_cast<uint32_t*>(ring + stage * A::kStage + A::kKSf + 4 * w) = 0;
+    }
+    __syncwarp();
+  }
+  int slots[kStages];  // of this tile's quad g and the following tiles'
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) slots[k] = slot_of(tile + k * kWarps);
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) fetch(tile + k * kWarps, slots[k], k);
 
   // queries: a warp a row, in the order that the lanes read them
-  constexpr int kEach = R / kWarps;
+  constexpr int kEach = R / kWarps;  // (a power of two)
   uint4 raw[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -295,8 +324,21 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
     l[n][0] = l[n][1] = l[n][2] = l[n][3] = 0.0f;
   }
 
+  int stage = 0;
   for (; tile < tile1; tile += kWarps) {
-    const int slot_after = slot_of(tile + 2 * kWarps);
+    copy_async_wait<kStages - 2>();
+    __syncwarp();  // this tile is there for all lanes, and the one before has been read by all
+    fetch(tile + (kStages - 1) * kWarps, slots[kStages - 1], stage == 0 ? kStages - 1 : stage - 1);
+    const int slot = slots[0];
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) slots[k] = slots[k + 1];
+    slots[kStages - 1] = slot_of(tile + kStages * kWarps);
+    const unsigned char* here = ring + stage * A::kStage;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
+    typename A::KFrag kf;
+    typename A::VFrag vf;
+    A::read_k(here, g, t, kf);
+    A::read_v_sf(here, g, t, vf);
     const int pos = position(tile);
     const int pos0 = pos - 4 * g;
     // ---- S^T = K Q^T
@@ -308,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
 #pragma unroll
     for (int jb = 0; jb < J; ++jb) {
       uint32_t sc[4];
-      const uint32_t sf = EXACT ? kf.sf[jb] : kf.sf[jb] & base.k_keep[jb];
+      const uint32_t sf = kf.sf[jb];
       e4m3x4_to_half2(__byte_perm(sf, 0, 0x1100), sc);
       e4m3x4_to_half2(__byte_perm(sf, 0, 0x3322), sc + 2);
 #pragma unroll
@@ -333,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
         }
       }
     }
-    fetch_k(slot_next);
 
     // ---- masks.  A NaN factor of V turns the weights of its slot NaN (for
     // the rows that see it) and counts as zero itself, so that it cannot reach
@@ -429,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
     }
 
     // ---- O^T += V^T P^T
+    A::read_v(here, g, t, vf);
     uint32_t sc[4];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -459,10 +501,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<HD, EXACT, NT>()) attn_kern
         }
       }
     }
-    fetch_v(slot_next);
-    slot = slot_next;
-    slot_next = slot_after;
   }
+  copy_async_wait<0>();
 
   // ---- the warps' parts joined
   if (g == 0) {
@@ -647,7 +687,9 @@ Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_le
   Plan p;
   const int64_t rows = (int64_t)max_q_len * (Hq / Hkv);
   const double pairs = (double)rows * Hkv * n_seqs * max_kv_len * hd / 128;
-  p.nt = rows >= kManyRows && pairs >= kManyPairs ? 0 : rows <= 8 ? 1 : rows <= 16 || hd > 128 ? 2 : 4;
+  // 32 rows to a CTA only where 16 would fill the GPU already
+  const bool small = (rows + 15) / 16 * Hkv * n_seqs * 8 < kSMs * 3;
+  p.nt = rows >= kManyRows && pairs >= kManyPairs ? 0 : rows <= 8 ? 1 : rows <= 16 || hd > 128 || small ? 2 : 4;
   const int tile_rows = p.nt == 0 ? kTileRows : 8 * p.nt;
   p.keys = p.nt == 0 ? tile_keys(hd) : kTile;
   const int64_t row_tiles = (rows + tile_rows - 1) / tile_rows;
@@ -655,10 +697,11 @@ Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_le
   const int64_t tiles = max_kv_len > 0 ? ((int64_t)max_kv_len + p.keys - 1) / p.keys : 1;
   const int64_t ctas = row_tiles * Hkv * n_seqs;
   // a CTA's smallest share: a tile for every warp
-  const int64_t least = p.nt == 0 ? 1 : kWarps;  // tiles
+  const int build = hd <= 64 ? 64 : hd <= 128 ? 128 : hd <= 192 ? 192 : 256;
+  const int64_t least = p.nt == 0 ? 1 : attn_warps(build, p.nt);  // tiles
   // CTAs that run at once; a batch of sequences, whose lengths differ, gets
   // four times as many
-  const int64_t want = (int64_t)kSMs * (p.nt == 0 ? (hd > 192 ? 1 : 2) : 4) * (n_seqs > 1 ? 4 : 1);
+  const int64_t want = (int64_t)kSMs * (p.nt == 0 ? (hd > 192 ? 1 : 2) : 16 / attn_warps(build, p.nt)) * (n_seqs > 1 ? 4 : 1);
   p.cluster = 0;
   p.chunks = 1;
   while (p.chunks < 8 && ctas * p.chunks * 2 <= want && tiles > p.chunks * least) p.chunks *= 2;
@@ -698,7 +741,7 @@ frt_status launch_attn(const Args& a, cudaStream_t stream) {
   static std::atomic<int> opted{48 * 1024};
   const frt_status st = opt_in_smem(attn_kernel<HD, EXACT, NT>, A::kSmem, opted);
   if (st != FRT_OK) return st;
-  const dim3 grid((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), block(kThreads);
+  const dim3 grid((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), block(A::kThreads);
   if (a.cluster) return launch_cluster(attn_kernel<HD, EXACT, NT>, grid, block, A::kSmem, stream, a.chunks, a);
   return launch(attn_kernel<HD, EXACT, NT>, grid, block, A::kSmem, stream, a);
 }
