@@ -103,19 +103,73 @@ struct Attn {
   static __device__ __forceinline__ int v_at(int row) { return kV + ((row & 7) * 4 + (row >> 3)) * kRow; }
   static __device__ __forceinline__ int v_swap(int row) { return J == 2 ? (row >> 4 & 1) * 32 : 0; }
 
+  // Where a lane copies from: its pieces of the slot of its row within a quad.
+  struct Source {
+    const uint8_t* k;
+    const uint8_t* sf;  // of K for the lanes below kHalf, of V above (HD 256: of K)
+    int64_t to_v, to_v_sf;
+    int row_bytes, sf_row;
+  };
+  static constexpr int kPieces = kRow / 16, kSfPieces = kSfRow / 16, kHalf = 8 * kSfPieces;
+  static __device__ __forceinline__ Source source(const Args& a, int kvh, int lane) {
+    Source s;
+    const int nblk = a.hd >> 4;
+    s.row_bytes = a.Hkv * (a.hd >> 1);
+    s.sf_row = a.Hkv * nblk;
+    s.k = a.k_codes + kvh * (a.hd >> 1);
+    s.sf = a.k_sf + kvh * nblk * 4;
+    s.to_v = a.v_codes - a.k_codes;
+    s.to_v_sf = a.v_sf - a.k_sf;
+    if (EXACT && 32 % kPieces == 0) {
+      s.k += (lane / kPieces & 3) * s.row_bytes + lane % kPieces * 16;
+      s.sf += lane % kSfPieces * 16;
+      if (lane >= kHalf) s.sf += s.to_v_sf;
+    }
+    return s;
+  }
+
   // Starts the copies of a tile: `slot` is the first slot of the lane's quad g
   // (-1: not there), `left` the positions from the tile's first to the end.
-  static __device__ __forceinline__ void fetch(const Args& a, int kvh, int slot, int left, int lane, uint32_t to) {
+  static __device__ __forceinline__ void fetch(const Args& a, const Source& src, int kvh, int slot, int left, int lane,
+                                               uint32_t to) {
+    const int64_t code_bytes = (int64_t)a.capacity * src.row_bytes;
+    const int64_t sf_bytes = (int64_t)((a.capacity + 3) >> 2) * src.sf_row * 4;
+    // the usual tile: every slot is there, no copy needs a condition
+    if (EXACT && 32 % kPieces == 0 && left >= kTile && !__any_sync(0xFFFFFFFFu, slot < 0)) {
+      const uint32_t to_k = to + k_at(lane / kPieces) + lane % kPieces * 16;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int row = 32 / kPieces * i + lane / kPieces;
+        const int quad = __shfl_sync(0xFFFFFFFFu, slot, row & ~3);  // lane 4 (row / 4)
+        const uint8_t* k = src.k + (int64_t)quad * src.row_bytes;
+        const uint8_t* v = k + src.to_v;
+        // rows a multiple of 4 on are that many quads on in K's order
+        if (32 / kPieces % 4 == 0)
+          copy_async<16>(to_k + 32 / kPieces / 4 * i * kRow, k, FRT_SPAN_OK(k - a.k_codes, 16, code_bytes));
+        else
+          copy_async<16>(to + k_at(row) + lane % kPieces * 16, k, FRT_SPAN_OK(k - a.k_codes, 16, code_bytes));
+        copy_async<16>(to + v_at(row) + (lane % kPieces * 16 ^ v_swap(row)), v,
+                       FRT_SPAN_OK(v - a.v_codes, 16, code_bytes));
+      }
+#pragma unroll
+      for (int i = 0; i < (2 * kHalf + 31) / 32; ++i) {
+        const int q = (32 * i + lane) % kHalf / kSfPieces;
+        const int quad = __shfl_sync(0xFFFFFFFFu, slot, 4 * q);
+        const uint8_t* f = src.sf + (int64_t)quad * src.sf_row + (i > 0 ? src.to_v_sf : 0);
+        const bool v_side = i > 0 || lane >= kHalf;
+        if (2 * kHalf % 32 == 0 || lane < 2 * kHalf)
+          copy_async<16>(to + (v_side ? kVSf : kKSf) + q * kSfRow + lane % kSfPieces * 16, f,
+                         FRT_SPAN_OK(f - (v_side ? a.v_sf : a.k_sf), 16, sf_bytes));
+      }
+      return;
+    }
     const int nblk = a.hd >> 4;
-    const int row_bytes = a.Hkv * (a.hd >> 1), sf_row = a.Hkv * nblk;
+    const int row_bytes = src.row_bytes, sf_row = src.sf_row;
     const uint8_t* k = a.k_codes + kvh * (a.hd >> 1);
     const uint8_t* v = a.v_codes + kvh * (a.hd >> 1);
     const uint8_t* k_sf = a.k_sf + kvh * nblk * 4;
     const uint8_t* v_sf = a.v_sf + kvh * nblk * 4;
-    const int64_t code_bytes = (int64_t)a.capacity * row_bytes;
-    const int64_t sf_bytes = (int64_t)((a.capacity + 3) >> 2) * sf_row * 4;
     if constexpr (EXACT) {
-      constexpr int kPieces = kRow / 16;  // of a row
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int row = (32 * i + lane) / kPieces, piece = (32 * i + lane) % kPieces * 16;
@@ -126,7 +180,6 @@ struct Attn {
         copy_async<16>(to + k_at(row) + piece, k + at, on);
         copy_async<16>(to + v_at(row) + (piece ^ v_swap(row)), v + at, on);
       }
-      constexpr int kSfPieces = kSfRow / 16, kHalf = 8 * kSfPieces;
 #pragma unroll
       for (int i = 0; i < (2 * kHalf + 31) / 32; ++i) {
         const int id = 32 * i + lane, q = id % kHalf / kSfPieces, piece = id % kSfPieces * 16;
@@ -247,12 +300,14 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
 
   // first loads, on their way while the queries are laid out
   unsigned char* ring = smem + warp * kStages * A::kStage;
+  const uint32_t ring_at = smem_addr(ring);
+  const typename A::Source source = A::source(a, kvh, lane);
   int tile = tile0 + warp;
   auto position = [&](int tl) { return rows.first() + tl * kTile + 4 * g; };
   auto slot_of = [&](int tl) { return tl < tile1 ? quad_slot(a, b, position(tl), rows) : -1; };
   auto fetch = [&](int tl, int slot, int stage) {
     if (tl < tile1)
-      A::fetch(a, kvh, slot, rows.all_hi - (rows.first() + tl * kTile), lane, smem_addr(ring + stage * A::kStage));
+      A::fetch(a, source, kvh, slot, rows.all_hi - (rows.first() + tl * kTile), lane, ring_at + stage * A::kStage);
     copy_async_commit();
   };
   if (!EXACT) {  // factors of blocks behind hd stay 0
@@ -269,6 +324,9 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
   for (int k = 0; k < kStages - 1; ++k) fetch(tile + k * kWarps, slots[k], k);
 
   // queries: a warp a row, in the order that the lanes read them
+  // (a negative scale changes their sign)
+  const float q_c = a.scale_log2 * gs_k;
+  const uint32_t flip = q_c < 0.0f ? 0x80008000u : 0u;
   constexpr int kEach = R / kWarps;  // (a power of two)
   uint4 raw[kEach];
 #pragma unroll
@@ -292,6 +350,7 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
       mul_pairs<4>(v, s);
       pack_pairs<FRT_F16, 4>(v, &raw[i].x);
     }
+    raw[i] = make_uint4(raw[i].x ^ flip, raw[i].y ^ flip, raw[i].z ^ flip, raw[i].w ^ flip);
     if (lane < HD / 8) {
       const int blk = lane >> 1;
       const int step = (blk % J) * 4 + (lane & 1) * 2;
@@ -299,12 +358,13 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
       dst[0] = make_uint2(raw[i].x, raw[i].y);
       dst[NT * 32] = make_uint2(raw[i].z, raw[i].w);
     }
-    if (lane == 0) q_scale[r] = a.scale_log2 * gs_k / s;
+    // (never 0, which would make a masked score NaN)
+    if (lane == 0) q_scale[r] = fmaxf(fabsf(q_c) / s, 0x1p-120f);
   }
   __syncthreads();
 
   const float kInf = __int_as_float(0x7F800000);
-  float c[NT][2], m[NT][2];
+  float c[NT][2], m[NT][2], shift[NT][2];
   int lo[NT][2], hi[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -313,6 +373,7 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
       const int r = 8 * n + 2 * t + e;
       c[n][e] = q_scale[r];
       m[n][e] = -kInf;
+      shift[n][e] = 11.0f;
       lo[n][e] = __shfl_sync(0xFFFFFFFFu, mine.lo, r);
       hi[n][e] = __shfl_sync(0xFFFFFFFFu, mine.hi, r);
     }
@@ -324,6 +385,9 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
     l[n][0] = l[n][1] = l[n][2] = l[n][3] = 0.0f;
   }
 
+  // tiles full0 .. full1 - 1 are seen whole by every row
+  const int full0 = (max(rows.full_lo - rows.first(), 0) + kTile - 1) / kTile;
+  const int full1 = max(rows.full_hi - rows.first(), 0) / kTile;
   int stage = 0;
   for (; tile < tile1; tile += kWarps) {
     copy_async_wait<kStages - 2>();
@@ -339,8 +403,6 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
     typename A::VFrag vf;
     A::read_k(here, g, t, kf);
     A::read_v_sf(here, g, t, vf);
-    const int pos = position(tile);
-    const int pos0 = pos - 4 * g;
     // ---- S^T = K Q^T
     float s[NT][8];
 #pragma unroll
@@ -379,12 +441,12 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
     // ---- masks.  A NaN factor of V turns the weights of its slot NaN (for
     // the rows that see it) and counts as zero itself, so that it cannot reach
     // other rows.
-    uint32_t bad = 0;
+    uint32_t odd = slot < 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < A::kVs; ++j) bad |= nan_factors(vf.sf[h][j]);
-    if (__any_sync(0xFFFFFFFFu, bad != 0)) {
+      for (int j = 0; j < A::kVs; ++j) odd |= nan_factors(vf.sf[h][j]);
+    if (__any_sync(0xFFFFFFFFu, odd != 0) || tile < full0 || tile >= full1) {
       uint32_t nan_slots = 0;  // bit 8t + 4h + i
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -400,26 +462,16 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
           if ((mark >> (8 * i + 7)) & 1) nan_slots |= 1u << (8 * t + 4 * h + i);
       }
       nan_slots = __reduce_or_sync(0xFFFFFFFFu, nan_slots);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((nan_slots >> (4 * g + i)) & 1) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            s[n][2 * i] = s[n][2 * i + 1] = __int_as_float(0x7FC00000);
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[n][e] *= c[n][e & 1];
-    if (pos0 < rows.full_lo || rows.full_hi - pos0 < kTile || __any_sync(0xFFFFFFFFu, slot < 0)) {
+      const int pos = position(tile);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int e = 0; e < 2; ++e) {
+            if ((nan_slots >> (4 * g + i)) & 1) s[n][2 * i + e] = __int_as_float(0x7FC00000);
             if (slot < 0 || pos + i < lo[n][e] || pos + i >= hi[n][e]) s[n][2 * i + e] = -kInf;
+          }
     }
 
     // ---- running maximum, renewed when a score passes it by more than 4
@@ -429,7 +481,7 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float top = fmaxf(fmaxf(s[n][e], s[n][2 + e]), fmaxf(s[n][4 + e], s[n][6 + e]));
-        above |= top > m[n][e] + 4.0f;
+        above |= fmaf(top, c[n][e], -4.0f) > m[n][e];
       }
     if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
@@ -439,9 +491,11 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
           float top = fmaxf(fmaxf(s[n][e], s[n][2 + e]), fmaxf(s[n][4 + e], s[n][6 + e]));
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          top *= c[n][e];
           if (top > m[n][e]) {
             const float f = ex2_approx(m[n][e] - top);
             m[n][e] = top;
+            shift[n][e] = 11.0f - top;
 #pragma unroll
             for (int i = 0; i < HD / 16; ++i) {
               o[n][i][e] *= f;
@@ -457,13 +511,11 @@ __global__ void __launch_bounds__(Attn<HD, EXACT, NT>::kThreads, Attn<HD, EXACT,
     uint32_t p[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float shift[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) shift[e] = (m[n][e] == -kInf ? 0.0f : m[n][e]) - 11.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        p[n][i] = transpose_8x8(Pack16<FRT_F16>::from_float2(ex2_approx(s[n][2 * i] - shift[0]),
-                                                             ex2_approx(s[n][2 * i + 1] - shift[1])));
+        p[n][i] = transpose_8x8(
+            Pack16<FRT_F16>::from_float2(ex2_approx(fmaf(s[n][2 * i], c[n][0], shift[n][0])),
+                                         ex2_approx(fmaf(s[n][2 * i + 1], c[n][1], shift[n][1]))));
       const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
       mma_16816(l[n], ones, p[n][0], p[n][1]);
       mma_16816(l[n], ones, p[n][2], p[n][3]);
