@@ -11,7 +11,9 @@
 // four groups of weights on their way (4 KB and their factors), which is what
 // covers the HBM latency.  Tiles are dealt to the CTAs in turn, so that the SMs'
 // shares differ by one tile at most; a warp takes a tile alone, or kw warps
-// split its k and join their sums in shared memory in a fixed order.
+// split its k and join their sums in shared memory in a fixed order.  Laying x
+// out costs every CTA its whole share of k: with many rows of x or few tiles the
+// CTAs of a cluster split k too, and join through distributed shared memory.
 //
 // x lies in shared memory as binary16 in the order in which the lanes read it
 // (16 bytes are a lane's part of two products).  FP16 rows, e4m3 codes and
@@ -26,11 +28,12 @@
 namespace frt {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 128;  // k of one load
-constexpr int kAhead = 4;    // groups a warp has on their way
 constexpr int kSMs = 148;
+// Warps of a CTA and groups that a warp has on their way.  Up to 16 rows of x
+// two CTAs share an SM, above there is one of twice the warps.
+__host__ __device__ constexpr int warps_of(int nt) { return nt <= 2 ? 8 : 16; }
+__host__ __device__ constexpr int ahead_of(int nt) { return nt <= 2 ? 4 : 2; }
 
 enum XForm { kX16, kXScaled16, kXE4M3, kXE4M3Block, kXNvfp4 };
 
@@ -49,6 +52,7 @@ struct Args {
   int seg_groups;  // groups of x in shared memory at a time
   int kw, kw_log2; // warps that share a weight tile (a power of two)
   int tiles;       // weight tiles of 16 rows
+  int cluster;     // CTAs that split k
   int swizzled;
   XForm form;
   int dt;
@@ -132,59 +136,86 @@ struct WRows {
   }
 };
 
-// Eight elements of row r (within the launch) from column k on: the raw bits,
-// and for NVFP4 their factor.
-struct XRaw {
-  uint4 v;
-  uint32_t sf;
-};
-__device__ __forceinline__ XRaw load_x(const Args& a, int r, int k) {
-  XRaw o;
-  o.v = make_uint4(0, 0, 0, 0);
-  o.sf = 0;
-  if (r >= a.rows || k >= a.K) return o;
-  const int64_t row = a.m0 + r;
-  const int64_t at = row * a.K + k, n = (int64_t)a.M * a.K;
-  if (!FRT_SPAN_OK(at, 8, n)) return o;
-  const uint8_t* x = static_cast<const uint8_t*>(a.x);
-  if (a.form == kX16 || a.form == kXScaled16) {
-    o.v = ld_plain(reinterpret_cast<const uint4*>(x + 2 * at));
-  } else if (a.form != kXNvfp4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(x + at);
-    o.v.x = u.x;
-    o.v.y = u.y;
-  } else {
-    o.v.x = *reinterpret_cast<const uint32_t*>(x + (at >> 1));
-    const int64_t sa = a.swizzled ? sf_offset_swizzled(row, k >> 4, a.K >> 4) : row * (a.K >> 4) + (k >> 4);
-    if (FRT_IDX_OK(sa, sf_bytes(a, a.M))) o.sf = a.x_sf[sa];
+// Lays rows of x out in shared memory as binary16, groups seg .. seg + len - 1
+// of n_rows rows (those behind the last are zeros): xf in the lanes' order, xs
+// the factors.  16 lanes take a group of a row, eight elements each; a row is
+// shared by `split` of these half-warps, whose loads go out in batches.
+template <XForm FORM, int NT, int kWarps>
+__device__ __forceinline__ void stage_x(const Args& a, int seg, int len, int n_rows, int mr, int step, uint4* xf,
+                                        float* xs) {
+  constexpr bool kScaled = FORM == kXScaled16 || FORM == kXE4M3Block;
+  constexpr int kBatch = 4;
+  constexpr int kBytes = FORM == kX16 || FORM == kXScaled16 ? 16 : FORM == kXNvfp4 ? 4 : 8;  // of eight elements
+  const int l = threadIdx.x & 15, h = threadIdx.x >> 4;
+  const int split = max(2 * kWarps / n_rows, 1), row_step = 2 * kWarps / split;
+  const int r0 = h / split, part = h - r0 * split;
+  const int64_t x_bytes = (int64_t)a.M * (a.K / 8) * kBytes;
+  // (trip counts are the same for both halves of a warp)
+  for (int j = 0; j < n_rows; j += row_step) {
+    const int r = r0 + j;
+    const bool row_on = r0 < row_step && r < n_rows, data = row_on && r < a.rows;
+    const int64_t row = a.m0 + min(r, a.rows - 1);
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + row * (a.K / 8) * kBytes + l * kBytes;
+    for (int c0 = part; c0 - part < len; c0 += kBatch * split) {
+      uint4 v[kBatch];
+      uint32_t sf[kBatch];
+      float scale[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int c = c0 + b * split, k = (seg + c) * kGroup + 8 * l;
+        v[b] = make_uint4(0, 0, 0, 0);
+        sf[b] = 0;
+        scale[b] = 1.0f;
+        if (data && c < len && k < a.K) {
+          const uint8_t* p = x + (int64_t)(seg + c) * (16 * kBytes);
+          if (!FRT_SPAN_OK(p - static_cast<const uint8_t*>(a.x), kBytes, x_bytes)) continue;
+          if (kBytes == 16) {
+            v[b] = *reinterpret_cast<const uint4*>(p);
+          } else if (kBytes == 8) {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            v[b].x = u.x;
+            v[b].y = u.y;
+          } else {
+            v[b].x = *reinterpret_cast<const uint32_t*>(p);
+          }
+          if (FORM == kXNvfp4) {
+            const int64_t at = a.swizzled ? sf_offset_swizzled(row, k >> 4, a.K >> 4) : row * (a.K >> 4) + (k >> 4);
+            if (FRT_IDX_OK(at, sf_bytes(a, a.M))) sf[b] = a.x_sf[at];
+          }
+          if (FORM == kXE4M3Block) {
+            const int64_t at = row * a.groups + seg + c;
+            if (FRT_IDX_OK(at, (int64_t)a.M * a.groups)) scale[b] = a.x_scales[at];
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int c = c0 + b * split;
+        uint4 o = v[b];
+        if (FORM == kXScaled16) {
+          float2 f[4];
+          unpack_pairs<FRT_BF16, 4>(&o.x, f);
+          const float amax = fmaxf(absmax4(f[0].x, f[0].y, f[1].x, f[1].y), absmax4(f[2].x, f[2].y, f[3].x, f[3].y));
+          const float s = pow2_to_half_range(half_warp_max_abs(amax));
+          mul_pairs<4>(f, s);
+          pack_pairs<FRT_F16, 4>(f, &o.x);
+          scale[b] = 1.0f / s;
+        } else if (FORM == kXE4M3 || FORM == kXE4M3Block) {
+          e4m3x4_to_half2(v[b].x, &o.x);
+          e4m3x4_to_half2(v[b].y, &o.z);
+        } else if (FORM == kXNvfp4) {
+          uint32_t f[2];
+          e2m1x8_to_half2(v[b].x, &o.x);
+          e4m3x4_to_half2(sf[b] * 0x0101u, f);
+          o = make_uint4(hmul2(o.x, f[0]), hmul2(o.y, f[0]), hmul2(o.z, f[0]), hmul2(o.w, f[0]));
+        }
+        if (row_on && c < len) {
+          xf[(c * 4 + (l & 3)) * step + ((r >> 3) * mr + (r & 7)) * 4 + (l >> 2)] = o;
+          if (kScaled && l == 0) xs[c * (8 * NT) + r] = scale[b];
+        }
+      }
+    }
   }
-  return o;
-}
-// The same as binary16; 16 lanes hold a group of a row, *scale is its factor.
-__device__ __forceinline__ uint4 convert_x(const Args& a, const XRaw& raw, int r, int group, float* scale) {
-  *scale = 1.0f;
-  uint4 o = raw.v;
-  if (a.form == kXScaled16) {
-    float2 v[4];
-    unpack_pairs<FRT_BF16, 4>(&o.x, v);
-    const float amax = fmaxf(absmax4(v[0].x, v[0].y, v[1].x, v[1].y), absmax4(v[2].x, v[2].y, v[3].x, v[3].y));
-    const float s = pow2_to_half_range(half_warp_max_abs(amax));
-    mul_pairs<4>(v, s);
-    pack_pairs<FRT_F16, 4>(v, &o.x);
-    *scale = 1.0f / s;
-  } else if (a.form == kXE4M3 || a.form == kXE4M3Block) {
-    const uint2 u = make_uint2(raw.v.x, raw.v.y);
-    e4m3x4_to_half2(u.x, &o.x);
-    e4m3x4_to_half2(u.y, &o.z);
-    const int64_t at = (int64_t)(a.m0 + r) * a.groups + group;
-    if (a.form == kXE4M3Block && r < a.rows && FRT_IDX_OK(at, (int64_t)a.M * a.groups)) *scale = a.x_scales[at];
-  } else if (a.form == kXNvfp4) {
-    uint32_t f[2];
-    e2m1x8_to_half2(raw.v.x, &o.x);
-    e4m3x4_to_half2(raw.sf * 0x0101u, f);
-    o = make_uint4(hmul2(o.x, f[0]), hmul2(o.y, f[0]), hmul2(o.z, f[0]), hmul2(o.w, f[0]));
-  }
-  return o;
 }
 
 template <int DT>
@@ -194,29 +225,91 @@ __device__ __forceinline__ float value16(uint16_t w) {
 
 constexpr int kRedStride = 20;  // floats between two rows of x of a warp's sums
 
+// y[row r][n] from its sum, scaled and with the bias.
+__device__ __forceinline__ void store_y1(const Args& a, int r, int n, float sum, float scale) {
+  const bool half = a.dt == FRT_F16;
+  float b = 0.0f;
+  if (a.bias != nullptr && FRT_IDX_OK(n, a.N)) b = half ? value16<FRT_F16>(a.bias[n]) : value16<FRT_BF16>(a.bias[n]);
+  const float v = fmaf(sum, scale, b);
+  const int64_t at = (int64_t)(a.m0 + r) * a.N + n;
+  if (FRT_IDX_OK(at, (int64_t)a.M * a.N))
+    a.y[at] = (uint16_t)(half ? Pack16<FRT_F16>::from_float2(v, 0.0f) : Pack16<FRT_BF16>::from_float2(v, 0.0f));
+}
+// y[row r][n .. n + 7]; N % 8 == 0 and y 16-byte aligned.
+__device__ __forceinline__ void store_y8(const Args& a, int r, int n, float* sum, float scale) {
+  const bool half = a.dt == FRT_F16;
+  float b[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (FRT_IDX_OK(n + e, a.N)) b[e] = half ? value16<FRT_F16>(a.bias[n + e]) : value16<FRT_BF16>(a.bias[n + e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = fmaf(sum[e], scale, b[e]);
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    out[e] = half ? Pack16<FRT_F16>::from_float2(sum[2 * e], sum[2 * e + 1])
+                  : Pack16<FRT_BF16>::from_float2(sum[2 * e], sum[2 * e + 1]);
+  const int64_t at = (int64_t)(a.m0 + r) * a.N + n;
+  if (FRT_SPAN_OK(at, 8, (int64_t)a.M * a.N))
+    *reinterpret_cast<uint4*>(a.y + at) = make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+__device__ __forceinline__ void add8(float* sum, const float4& u, const float4& v) {
+  sum[0] += u.x;
+  sum[1] += u.y;
+  sum[2] += u.z;
+  sum[3] += u.w;
+  sum[4] += v.x;
+  sum[5] += v.y;
+  sum[6] += v.z;
+  sum[7] += v.w;
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
 // Floats of a warp's sums of a tile, [row of x][weight row].
 __host__ __device__ constexpr int sum_floats(int nt, int mr) { return (nt == 1 ? mr : 8 * nt) * kRedStride; }
 
 // SCALED: x has a factor per row and group.
 template <int NT, bool SCALED, int LAY>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const Args a) {
+__global__ void __launch_bounds__(32 * warps_of(NT), NT <= 2 ? 2 : 1) matvec_kernel(const Args a) {
+  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps, kAhead = ahead_of(NT);
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int mr = NT == 1 ? min(a.rows, 8) : 8;  // rows of x that shared memory holds per 8
   const int step = NT * mr * 4;                 // 16-byte words of 32 k
   const int red_warp = sum_floats(NT, mr);
-  float* red = reinterpret_cast<float*>(smem);  // [2][warp][row of x][weight row]
-  uint4* xf = reinterpret_cast<uint4*>(smem + sizeof(float) * 2 * kWarps * red_warp);
+  const int ranks = a.cluster, rank = (int)blockIdx.x % ranks;
+  const int cta = (int)blockIdx.x / ranks, ctas = (int)gridDim.x / ranks;  // (clusters, if there are any)
+  const int kw = a.kw, ks = warp & (kw - 1), rw = warp >> a.kw_log2, at_once = kWarps >> a.kw_log2;
+  // the tile of this warp in a round (tiles are dealt to the CTAs in turn)
+  auto tile_of = [&](int round) { return (round * at_once + rw) * ctas + cta; };
+  const int per_round = at_once * ctas;
+  const int rounds = a.tiles / per_round + (a.tiles % per_round > cta);  // of this CTA's first warp
+  const int group0 = a.groups * rank / ranks, group1 = a.groups * (rank + 1) / ranks;
+
+  // sums [round, or its parity where there is no cluster][warp][row of x][weight row]
+  float* red = reinterpret_cast<float*>(smem);
+  const int sum_sets = ranks > 1 ? (a.tiles + per_round - 1) / per_round : 2;
+  uint4* xf = reinterpret_cast<uint4*>(smem + sizeof(float) * sum_sets * kWarps * red_warp);
   float* xs = reinterpret_cast<float*>(xf + (size_t)a.seg_groups * 4 * step);
   // rows of x that are not there: the last one again, its sums are dropped
   const uint4* x_lane = xf + min(g, mr - 1) * 4 + t;
-
-  const int kw = a.kw, ks = warp & (kw - 1), rw = warp >> a.kw_log2, at_once = kWarps >> a.kw_log2;
-  // the tile of this warp in a round (tiles are dealt to the CTAs in turn)
-  auto tile_of = [&](int round) { return (round * at_once + rw) * (int)gridDim.x + (int)blockIdx.x; };
-  const int per_round = at_once * (int)gridDim.x;
-  const int rounds = a.tiles / per_round + (a.tiles % per_round > (int)blockIdx.x);  // of this CTA's first warp
 
   // This warp's groups: of each tile and segment of k a contiguous share, in
   // sets of kAhead.  end == 0: no more.
@@ -224,65 +317,60 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
     int round, seg, base, end;
   };
   auto share = [&](Cursor& c) {
-    const int len = min(a.seg_groups, a.groups - c.seg);
+    const int len = min(a.seg_groups, group1 - c.seg);
     c.base = c.seg + (len * ks >> a.kw_log2);
     c.end = c.seg + (len * (ks + 1) >> a.kw_log2);
     if (tile_of(c.round) >= a.tiles) c.end = 0;
   };
-  auto advance = [&](Cursor c) {
-    c.base += kAhead;
+  auto settle = [&](Cursor& c) {  // past empty shares
     while (c.base >= c.end && c.end > 0) {
       c.seg += a.seg_groups;
-      if (c.seg >= a.groups) {
-        c.seg = 0;
+      if (c.seg >= group1) {
+        c.seg = group0;
         ++c.round;
       }
       share(c);
     }
+  };
+  auto advance = [&](Cursor c) {
+    c.base += kAhead;
+    settle(c);
     return c;
   };
   auto is_whole = [&](const Cursor& c) { return LAY != 0 && (c.base + kAhead) * kGroup <= a.K; };
   WFrag w[kAhead];
   WRows<LAY> rows;
-  Cursor cur = {0, 0, 0, 0};
+  Cursor cur = {0, group0, 0, 0};
   share(cur);
-  rows.set(a, tile_of(0) * 16, g);
+  settle(cur);
+  rows.set(a, tile_of(cur.round) * 16, g);
 #pragma unroll
   for (int u = 0; u < kAhead; ++u)
     if (cur.base + u < cur.end) rows.load(a, cur.base, u, is_whole(cur), t, w[u]);  // constant inputs: before the wait
   const float w_scale = __ldg(a.w_scale);
   pdl_enter();
+  const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
   const float scale = w_scale * (a.form == kXE4M3 || a.form == kXNvfp4 ? a.x_scales[0] : 1.0f);
 
   for (int round = 0; round < rounds; ++round) {
     float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-    for (int seg = 0; seg < a.groups; seg += a.seg_groups) {
-      if (a.seg_groups < a.groups || round == 0) {
-        if (seg > 0 || round > 0) __syncthreads();  // the last segment is read
-        const int n_rows = NT == 1 ? mr : 8 * NT;
-        const int n = n_rows * min(a.seg_groups, a.groups - seg);  // (row, group) pairs, one to 16 lanes
-        constexpr int kBatch = 4;
-        for (int i0 = warp * 2; i0 < n; i0 += 2 * kWarps * kBatch) {
-          XRaw raw[kBatch];
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * 2 * kWarps + (lane >> 4);
-            const int c = i / n_rows, r = i - c * n_rows;
-            raw[b] = load_x(a, i < n ? r : a.rows, (seg + c) * kGroup + 8 * (lane & 15));
-          }
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * 2 * kWarps + (lane >> 4);
-            const int c = i / n_rows, r = i - c * n_rows;
-            float s;
-            const uint4 v = convert_x(a, raw[b], i < n ? r : a.rows, seg + c, &s);
-            if (i < n) {
-              xf[(c * 4 + (lane & 3)) * step + ((r >> 3) * mr + (r & 7)) * 4 + ((lane & 15) >> 2)] = v;
-              if (SCALED && (lane & 15) == 0) xs[c * (8 * NT) + r] = s;
-            }
-          }
+    for (int seg = group0; seg < group1; seg += a.seg_groups) {
+      if (a.seg_groups < group1 - group0 || round == 0) {
+        if (seg > group0 || round > 0) __syncthreads();  // the last segment is read
+        const int n_rows = NT == 1 ? mr : 8 * NT, len = min(a.seg_groups, group1 - seg);
+        if (SCALED) {
+          if (a.form == kXScaled16)
+            stage_x<kXScaled16, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+          else
+            stage_x<kXE4M3Block, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+        } else if (a.form == kX16) {
+          stage_x<kX16, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+        } else if (a.form == kXE4M3) {
+          stage_x<kXE4M3, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+        } else {
+          stage_x<kXNvfp4, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
         }
         __syncthreads();
       }
@@ -339,8 +427,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
       }
     }
     // The sums through shared memory: of the warp's own tile, or of the kw warps
-    // that share one.  Two sets of them, so that one barrier a round is enough.
-    float* sums = red + (size_t)(round & 1) * kWarps * red_warp;
+    // that share one.  Two sets of them, so that one barrier a round is enough;
+    // a cluster keeps those of every round.
+    float* sums = red + (size_t)(ranks > 1 ? round : round & 1) * kWarps * red_warp;
     float* mine = sums + warp * red_warp + g;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -352,114 +441,141 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) matvec_kernel(const
           mine[r * kRedStride + 8] = acc[n][2 + e];
         }
       }
+    if (ranks > 1) continue;
     if (kw == 1)
       __syncwarp();
     else
       __syncthreads();
-    const int first = kw == 1 ? lane : threadIdx.x, threads = kw == 1 ? 32 : kThreads;
-    const int my_tiles = kw == 1 ? 1 : at_once;
-    const bool half = a.dt == FRT_F16;
-    if (NT == 1) {  // one output to a thread, neighbours along n
-      for (int i = first; i < my_tiles * 16 * a.rows; i += threads) {
-        const int col = i & 15, j = (i >> 4) & (my_tiles - 1), r = (i >> 4) / my_tiles;
-        const int q = kw == 1 ? rw : j;
-        const int n = ((round * at_once + q) * (int)gridDim.x + (int)blockIdx.x) * 16 + col;
-        if (n >= a.N) continue;
-        const float* p = sums + (q << a.kw_log2) * red_warp + r * kRedStride + col;
-        float sum = 0.0f;
-        for (int k = 0; k < kw; ++k) sum += p[k * red_warp];
-        sum *= scale;
-        if (a.bias != nullptr && FRT_IDX_OK(n, a.N))
-          sum += half ? value16<FRT_F16>(a.bias[n]) : value16<FRT_BF16>(a.bias[n]);
-        const int64_t at = (int64_t)(a.m0 + r) * a.N + n;
-        if (FRT_IDX_OK(at, (int64_t)a.M * a.N))
-          a.y[at] = (uint16_t)(half ? Pack16<FRT_F16>::from_float2(sum, 0.0f) : Pack16<FRT_BF16>::from_float2(sum, 0.0f));
+    if (NT == 1 || !wide) {  // one output to a lane, neighbours along n: two tiles, or two rows of a warp's own
+      const int two = lane >> 4, col = lane & 15;
+      const int r0 = kw == 1 ? two : warp, r_step = kw == 1 ? 2 : kWarps;
+      for (int r = r0; r < a.rows; r += r_step) {
+        for (int q = kw == 1 ? rw : two; q < at_once; q += kw == 1 ? kWarps : 2) {
+          const int n = ((round * at_once + q) * ctas + cta) * 16 + col;
+          if (n >= a.N) break;
+          const float* p = sums + (q << a.kw_log2) * red_warp + r * kRedStride + col;
+          float sum = 0.0f;
+          for (int k = 0; k < kw; ++k) sum += p[k * red_warp];
+          store_y1(a, r, n, sum, scale);
+        }
       }
       continue;
     }
-    const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-    for (int i = first; i < my_tiles * 2 * a.rows; i += threads) {
-      const int o = i & 1, j = (i >> 1) & (my_tiles - 1), r = (i >> 1) / my_tiles;
-      const int q = kw == 1 ? rw : j;
-      const int n = ((round * at_once + q) * (int)gridDim.x + (int)blockIdx.x) * 16 + 8 * o;
-      if (n >= a.N) continue;
-      float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      for (int k = 0; k < kw; ++k) {
-        const float* p = sums + ((q << a.kw_log2) + k) * red_warp + r * kRedStride + 8 * o;
-        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
-        sum[0] += u.x;
-        sum[1] += u.y;
-        sum[2] += u.z;
-        sum[3] += u.w;
-        sum[4] += v.x;
-        sum[5] += v.y;
-        sum[6] += v.z;
-        sum[7] += v.w;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum[e] *= scale;
-        if (a.bias != nullptr && n + e < a.N && FRT_IDX_OK(n + e, a.N)) {
-          const uint16_t b = a.bias[n + e];
-          sum[e] += half ? value16<FRT_F16>(b) : value16<FRT_BF16>(b);
+    // eight outputs to a lane: two lanes a tile and row of x, the rows dealt to
+    // the warps (of a warp's own tile to its lanes)
+    const int q = kw == 1 ? rw : lane >> 1, o = lane & 1;
+    const int n = ((round * at_once + q) * ctas + cta) * 16 + 8 * o;
+    if (q < at_once && n < a.N) {
+      const float* p = sums + (q << a.kw_log2) * red_warp + 8 * o;
+      for (int r = kw == 1 ? lane >> 1 : warp; r < a.rows; r += kw == 1 ? 16 : kWarps) {
+        float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < kw; ++k) {
+          const float* pk = p + k * red_warp + r * kRedStride;
+          add8(sum, *reinterpret_cast<const float4*>(pk), *reinterpret_cast<const float4*>(pk + 4));
         }
-      }
-      uint32_t out[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        out[e] = half ? Pack16<FRT_F16>::from_float2(sum[2 * e], sum[2 * e + 1])
-                      : Pack16<FRT_BF16>::from_float2(sum[2 * e], sum[2 * e + 1]);
-      const int64_t at = (int64_t)(a.m0 + r) * a.N + n;
-      if (wide) {
-        if (FRT_SPAN_OK(at, 8, (int64_t)a.M * a.N))
-          *reinterpret_cast<uint4*>(a.y + at) = make_uint4(out[0], out[1], out[2], out[3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < a.N && FRT_IDX_OK(at + e, (int64_t)a.M * a.N))
-            a.y[at + e] = (uint16_t)(out[e >> 1] >> (16 * (e & 1)));
+        store_y8(a, r, n, sum, scale);
       }
     }
   }
+  if (ranks == 1) return;
+
+  // ---- a cluster's sums: its tiles are dealt to the CTAs in turn; a lane reads
+  // the sums of one CTA (eight outputs), the lanes of a row are added as a tree
+  cluster_barrier();
+  const int slots = rounds * at_once;
+  const int c = (lane >> 1) & (ranks - 1), lanes = 2 * ranks;
+  const uint32_t red_at = cluster_address(smem_addr(red), c);
+  for (int j0 = 0; j0 * ranks + rank < slots; j0 += 32 / lanes) {
+    const int slot = (j0 + lane / lanes) * ranks + rank, n = (slot * ctas + cta) * 16 + 8 * (lane & 1);
+    const bool on = slot < slots && n < a.N;
+    for (int r = warp; r < a.rows; r += kWarps) {
+      const uint32_t at = red_at + (slot * kw * red_warp + r * kRedStride + 8 * (lane & 1)) * 4;
+      float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (on)
+        for (int k = 0; k < kw; ++k) {
+          const float4 u = ld_cluster(at + k * red_warp * 4), v = ld_cluster(at + k * red_warp * 4 + 16);
+          add8(sum, u, v);
+        }
+      for (int d = 2; d < lanes; d *= 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], d);
+      if (on && c == 0) {
+        if (wide) {
+          store_y8(a, r, n, sum, scale);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < a.N) store_y1(a, r, n + e, sum[e], scale);
+        }
+      }
+    }
+  }
+  cluster_barrier();  // the sums are read
 }
 
 template <int NT, bool SCALED, int LAY>
 frt_status launch_one(Args a, cudaStream_t stream) {
-  constexpr int kPerSM = NT <= 2 ? 2 : 1;
+  constexpr int kPerSM = NT <= 2 ? 2 : 1, kWarps = warps_of(NT), kAhead = ahead_of(NT);
   a.tiles = (int)(((int64_t)a.N + 15) / 16);
   const int mr = NT == 1 && a.rows < 8 ? a.rows : 8;
+  const int x_rows = NT == 1 ? mr : 8 * NT;
   const size_t group_bytes = (size_t)4 * NT * mr * 4 * 16 + (SCALED ? 8 * NT * 4 : 0);
-  const size_t red = sizeof(float) * 2 * kWarps * sum_floats(NT, mr);
-  // all of x in shared memory where it fits, with the CTAs that share an SM
-  // where that fits
-  const size_t all = red + a.groups * group_bytes;
-  const int per_sm = all <= 112 * 1024 ? kPerSM : 1;
-  const int fit = (int)std::min<size_t>((225 * 1024 - red) / group_bytes, a.groups);
-  // warps to a tile: the fewest rounds, a round being its share of k and the
-  // cost of a round itself (about a group and a half)
-  int64_t best = 0;
-  for (int kw = 1, log2 = 0; kw <= kWarps && kw <= a.groups; kw *= 2, ++log2) {
-    const int64_t slots = (int64_t)kSMs * per_sm * (kWarps / kw);
-    const int64_t rounds = (a.tiles + slots - 1) / slots;
-    const int64_t cost = rounds * (2 * ((a.groups + kw - 1) / kw) + 3);
-    if (kw == 1 || cost < best) {
-      best = cost;
-      a.kw = kw;
-      a.kw_log2 = log2;
+  const size_t set_bytes = sizeof(float) * kWarps * sum_floats(NT, mr);
+  const size_t most = 225 * 1024, half = 112 * 1024;
+  // How k is split, over the kw warps that share a tile and the CTAs of a
+  // cluster: the cheapest of the plans that fit, in microseconds.  Measured: a
+  // batch of x 0.8; a group (0.25 + 0.1 NT)
+  // for a warp among up to 16 of the SM; a round 0.5; joining a cluster's sums 2.5
+  // and 0.2 (1 + kw) for every turn of a warp.
+  double best = 0;
+  size_t smem = 0;
+  int per_sm = 1;
+  a.cluster = 0;
+  for (int ranks = 1; ranks <= 8; ranks *= 2) {
+    if (ranks > 1 && ranks > a.groups) break;
+    const int k_groups = (a.groups + ranks - 1) / ranks;
+    for (int kw = 1, log2 = 0; kw <= kWarps && kw <= k_groups; kw *= 2, ++log2) {
+      for (int sm = kPerSM; sm >= 1; --sm) {
+        const int64_t ctas = kSMs * sm / ranks;
+        const int64_t used = a.tiles < ctas ? a.tiles : ctas;
+        const int64_t per_round = used * (kWarps / kw);
+        const int64_t rounds = (a.tiles + per_round - 1) / per_round;
+        const size_t red = set_bytes * (ranks > 1 ? (size_t)rounds : 2);
+        const size_t limit = sm == 2 ? half : most;
+        int seg = k_groups;
+        if (red + k_groups * group_bytes > limit) {
+          // x in segments, whole sets for every warp; not in a cluster
+          if (ranks > 1 || sm == 2 || red + kw * kAhead * group_bytes > limit) continue;
+          seg = (int)((limit - red) / group_bytes) / (kw * kAhead) * (kw * kAhead);
+        }
+        const int split = 2 * kWarps / x_rows > 1 ? 2 * kWarps / x_rows : 1;
+        const int turns_x = (x_rows + 2 * kWarps / split - 1) / (2 * kWarps / split);
+        const double batches = (double)turns_x * ((seg + 4 * split - 1) / (4 * split));
+        const double staging = 0.8 * batches * (seg < k_groups ? (double)((k_groups + seg - 1) / seg * rounds) : 1.0);
+        const double group = 0.25 + 0.1 * NT;
+        const double turns = (double)((a.rows + kWarps - 1) / kWarps) * (double)((rounds * (kWarps / kw) + 15) / 16);
+        const double cost = staging + rounds * (((k_groups + kw - 1) / kw) * group + 0.5) +
+                            (ranks > 1 ? 2.5 + turns * (0.2 + 0.2 * kw) : 0.0);
+        if (a.cluster == 0 || cost < best) {
+          best = cost;
+          a.cluster = ranks;
+          a.kw = kw;
+          a.kw_log2 = log2;
+          a.seg_groups = seg;
+          per_sm = sm;
+          smem = red + seg * group_bytes;
+        }
+      }
     }
   }
-  while (fit < a.groups && a.kw * kAhead > fit) {  // a segment is whole sets for every warp
-    a.kw /= 2;
-    --a.kw_log2;
-  }
-  a.seg_groups = fit >= a.groups ? a.groups : fit / (a.kw * kAhead) * (a.kw * kAhead);
-  const size_t smem = red + a.seg_groups * group_bytes;
+  if (a.cluster == 0) return FRT_ERR_UNSUPPORTED;  // (never: a segment of one set always fits)
   static std::atomic<int> opted{48 * 1024};
   const frt_status st = opt_in_smem(matvec_kernel<NT, SCALED, LAY>, smem, opted);
   if (st != FRT_OK) return st;
-  const int ctas = kSMs * per_sm;
-  const unsigned grid = (unsigned)(a.tiles < ctas ? a.tiles : ctas);
-  return launch(matvec_kernel<NT, SCALED, LAY>, dim3(grid), dim3(kThreads), smem, stream, a);
+  const int ctas = kSMs * per_sm / a.cluster;
+  const dim3 grid((unsigned)((a.tiles < ctas ? a.tiles : ctas) * a.cluster)), block(32 * kWarps);
+  if (a.cluster > 1) return launch_cluster(matvec_kernel<NT, SCALED, LAY>, grid, block, smem, stream, a.cluster, a);
+  return launch(matvec_kernel<NT, SCALED, LAY>, grid, block, smem, stream, a);
 }
 template <int NT, bool SCALED>
 frt_status launch_layout(const Args& a, cudaStream_t stream) {
