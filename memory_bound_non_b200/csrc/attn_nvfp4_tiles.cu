@@ -160,7 +160,7 @@ struct Small {  // behind the operands
   uint32_t nan[4];            // keys of the tile with a NaN factor in V
   float2 ml[kTileRows];       // (maximum, sum) of a row, for the cluster
   float factor[8][kTileRows];
-  uint64_t s_done, o_done;
+  uint64_t s_done, o_done, drained;
   uint32_t tmem;
   int gave_up;
 };
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
   if (threadIdx.x == 0) {
     mbar_init(&sm.s_done, 1);
     mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.drained, 1);
     mbar_init_fence();
     sm.gave_up = 0;
   }
@@ -514,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
   // a wait that ran out: report it, and let the products end before TMEM is freed
   if (sm.gave_up != 0 && threadIdx.x == 0) {
     if (a.status != nullptr) atomicOr(a.status, 2);
-    if (n > 0) (void)mbar_wait_bounded(&sm.o_done, (n - 1) & 1, 1 << 16);
+    tc_commit(&sm.drained);
+    (void)mbar_wait_bounded(&sm.drained, 0, 1 << 16);
   }
   __syncwarp();
   tc_fence_before();

@@ -293,13 +293,13 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// Power of two that brings magnitude amax (> 0, finite) into [2^14, 2^15),
-// within 2^-100 .. 2^100; 1 for zero, infinite and NaN amax.
+// Power of two that brings magnitude amax (> 0, finite) into [2^14, 2^15), at
+// most 2^127 (below 2^-113 the bf16 numbers, multiples of 2^-133, are exact in
+// binary16 all the same); 1 for zero, infinite and NaN amax.
 __device__ __forceinline__ float pow2_to_half_range(float amax) {
   const int e = (int)(__float_as_uint(amax) >> 23) - 127;  // amax >= 0; subnormals count as 2^-127
   if (!(amax > 0.0f) || e == 128) return 1.0f;
-  const int k = 14 - e;
-  return __int_as_float((min(max(k, -100), 100) + 127) << 23);
+  return __int_as_float((min(14 - e, 127) + 127) << 23);  // (14 - e >= -113)
 }
 
 // ------------------------------------------------------------ memory ops --

@@ -138,11 +138,11 @@ struct WRows {
 
 // Lays rows of x out in shared memory as binary16, groups seg .. seg + len - 1
 // of n_rows rows (those behind the last are zeros): xf in the lanes' order, xs
-// the factors.  16 lanes take a group of a row, eight elements each; a row is
+// the factors times the weights' scale.  16 lanes take a group of a row, eight elements each; a row is
 // shared by `split` of these half-warps, whose loads go out in batches.
 template <XForm FORM, int NT, int kWarps>
-__device__ __forceinline__ void stage_x(const Args& a, int seg, int len, int n_rows, int mr, int step, uint4* xf,
-                                        float* xs) {
+__device__ __forceinline__ void stage_x(const Args& a, int seg, int len, int n_rows, int mr, int step, float w_scale,
+                                        uint4* xf, float* xs) {
   constexpr bool kScaled = FORM == kXScaled16 || FORM == kXE4M3Block;
   constexpr int kBatch = 4;
   constexpr int kBytes = FORM == kX16 || FORM == kXScaled16 ? 16 : FORM == kXNvfp4 ? 4 : 8;  // of eight elements
@@ -211,7 +211,7 @@ __device__ __forceinline__ void stage_x(const Args& a, int seg, int len, int n_r
         }
         if (row_on && c < len) {
           xf[(c * 4 + (l & 3)) * step + ((r >> 3) * mr + (r & 7)) * 4 + (l >> 2)] = o;
-          if (kScaled && l == 0) xs[c * (8 * NT) + r] = scale[b];
+          if (kScaled && l == 0) xs[c * (8 * NT) + r] = scale[b] * w_scale;
         }
       }
     }
@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(32 * warps_of(NT), NT <= 2 ? 2 : 1) matvec_ker
   const float w_scale = __ldg(a.w_scale);
   pdl_enter();
   const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-  const float scale = w_scale * (a.form == kXE4M3 || a.form == kXNvfp4 ? a.x_scales[0] : 1.0f);
+  // (the weights' scale is in xs where there are such factors: sums of large rows stay finite)
+  const float scale = SCALED ? 1.0f : w_scale * (a.form == kX16 ? 1.0f : a.x_scales[0]);
 
   for (int round = 0; round < rounds; ++round) {
     float acc[NT][4];
@@ -362,15 +363,15 @@ __global__ void __launch_bounds__(32 * warps_of(NT), NT <= 2 ? 2 : 1) matvec_ker
         const int n_rows = NT == 1 ? mr : 8 * NT, len = min(a.seg_groups, group1 - seg);
         if (SCALED) {
           if (a.form == kXScaled16)
-            stage_x<kXScaled16, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+            stage_x<kXScaled16, NT, kWarps>(a, seg, len, n_rows, mr, step, w_scale, xf, xs);
           else
-            stage_x<kXE4M3Block, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+            stage_x<kXE4M3Block, NT, kWarps>(a, seg, len, n_rows, mr, step, w_scale, xf, xs);
         } else if (a.form == kX16) {
-          stage_x<kX16, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+          stage_x<kX16, NT, kWarps>(a, seg, len, n_rows, mr, step, w_scale, xf, xs);
         } else if (a.form == kXE4M3) {
-          stage_x<kXE4M3, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+          stage_x<kXE4M3, NT, kWarps>(a, seg, len, n_rows, mr, step, w_scale, xf, xs);
         } else {
-          stage_x<kXNvfp4, NT, kWarps>(a, seg, len, n_rows, mr, step, xf, xs);
+          stage_x<kXNvfp4, NT, kWarps>(a, seg, len, n_rows, mr, step, w_scale, xf, xs);
         }
         __syncthreads();
       }
