@@ -4,6 +4,7 @@
 
 #include "frt_device.cuh"
 #include "frt_host.h"
+#include "frt_tensor.cuh"
 
 namespace frt {
 
@@ -147,26 +148,6 @@ __device__ __forceinline__ int quad_slot(const AttnArgs& a, int b, int pos, cons
 // Bytes that hold the NaN factor, marked in their top bits.
 __device__ __forceinline__ uint32_t nan_factors(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-}
-
-// Cluster-wide barrier, and loads from the shared memory of its CTA `rank`.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
-  return v;
 }
 
 // Four outputs from d on, and the part of a chunk.

@@ -272,6 +272,12 @@ __device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t* h) {
       : "=r"(h[0]), "=r"(h[1])
       : "r"(w));
 }
+// One e4m3 code in both halves.
+__device__ __forceinline__ uint32_t e4m3_to_both(uint32_t code) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 w;\n\tcvt.u16.u32 w, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, w;\n\t}" : "=r"(h) : "r"(code * 0x0101u));
+  return h;
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));

@@ -22,46 +22,19 @@
 // and group that is applied to the group's fp32 sums.
 #include <algorithm>
 
-#include "frt_device.cuh"
-#include "frt_host.h"
+#include "matvec_nvfp4.cuh"
 
 namespace frt {
 namespace {
 
-constexpr int kGroup = 128;  // k of one load
 constexpr int kSMs = 148;
-// Warps of a CTA and groups that a warp has on their way.  Up to 16 rows of x
-// two CTAs share an SM, above there is one of twice the warps.
-__host__ __device__ constexpr int warps_of(int nt) { return nt <= 2 ? 8 : 16; }
-__host__ __device__ constexpr int ahead_of(int nt) { return nt <= 2 ? 4 : 2; }
+constexpr int kAhead = 4;  // groups a warp has on their way
+// CTAs that share an SM and their warps: up to 8 rows of x two, above one of
+// twice the warps, which lays its many rows out once.
+__host__ __device__ constexpr int ctas_of(int nt) { return nt == 1 ? 2 : 1; }
+__host__ __device__ constexpr int warps_of(int nt) { return 16 / ctas_of(nt); }
 
-enum XForm { kX16, kXScaled16, kXE4M3, kXE4M3Block, kXNvfp4 };
-
-struct Args {
-  const void* x;
-  const float* x_scales;
-  const uint8_t* x_sf;
-  const uint8_t* w_codes;
-  const uint8_t* w_sf;
-  const float* w_scale;
-  const uint16_t* bias;
-  uint16_t* y;
-  int M, N, K;
-  int m0, rows;    // rows of x of this launch: m0 .. m0 + rows - 1
-  int groups;      // ceil(K / 128)
-  int seg_groups;  // groups of x in shared memory at a time
-  int kw, kw_log2; // warps that share a weight tile (a power of two)
-  int tiles;       // weight tiles of 16 rows
-  int cluster;     // CTAs that split k
-  int swizzled;
-  XForm form;
-  int dt;
-};
-
-__device__ __forceinline__ int64_t sf_bytes(const Args& a, int64_t n_rows) {
-  const int cols = a.K >> 4;
-  return a.swizzled ? ((n_rows + 127) >> 7) * (int64_t)((cols + 3) >> 2) * 512 : n_rows * cols;
-}
+using Args = MatvecArgs;
 
 // Weights of one group: rows g and g + 8, 32 codes and two factors each.
 struct WFrag {
@@ -218,23 +191,8 @@ __device__ __forceinline__ void stage_x(const Args& a, int seg, int len, int n_r
   }
 }
 
-template <int DT>
-__device__ __forceinline__ float value16(uint16_t w) {
-  return Pack16<DT>::to_float2((uint32_t)w).x;
-}
-
 constexpr int kRedStride = 20;  // floats between two rows of x of a warp's sums
 
-// y[row r][n] from its sum, scaled and with the bias.
-__device__ __forceinline__ void store_y1(const Args& a, int r, int n, float sum, float scale) {
-  const bool half = a.dt == FRT_F16;
-  float b = 0.0f;
-  if (a.bias != nullptr && FRT_IDX_OK(n, a.N)) b = half ? value16<FRT_F16>(a.bias[n]) : value16<FRT_BF16>(a.bias[n]);
-  const float v = fmaf(sum, scale, b);
-  const int64_t at = (int64_t)(a.m0 + r) * a.N + n;
-  if (FRT_IDX_OK(at, (int64_t)a.M * a.N))
-    a.y[at] = (uint16_t)(half ? Pack16<FRT_F16>::from_float2(v, 0.0f) : Pack16<FRT_BF16>::from_float2(v, 0.0f));
-}
 // y[row r][n .. n + 7]; N % 8 == 0 and y 16-byte aligned.
 __device__ __forceinline__ void store_y8(const Args& a, int r, int n, float* sum, float scale) {
   const bool half = a.dt == FRT_F16;
@@ -267,27 +225,13 @@ __device__ __forceinline__ void add8(float* sum, const float4& u, const float4& 
   sum[7] += v.w;
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-  return v;
-}
-
 // Floats of a warp's sums of a tile, [row of x][weight row].
 __host__ __device__ constexpr int sum_floats(int nt, int mr) { return (nt == 1 ? mr : 8 * nt) * kRedStride; }
 
 // SCALED: x has a factor per row and group.
 template <int NT, bool SCALED, int LAY>
-__global__ void __launch_bounds__(32 * warps_of(NT), NT <= 2 ? 2 : 1) matvec_kernel(const Args a) {
-  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps, kAhead = ahead_of(NT);
+__global__ void __launch_bounds__(32 * warps_of(NT), ctas_of(NT)) matvec_kernel(const Args a) {
+  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps;
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -482,10 +426,10 @@ __global__ void __launch_bounds__(32 * warps_of(NT), NT <= 2 ? 2 : 1) matvec_ker
 
   // ---- a cluster's sums: its tiles are dealt to the CTAs in turn; a lane reads
   // the sums of one CTA (eight outputs), the lanes of a row are added as a tree
-  cluster_barrier();
+  cluster_sync();
   const int slots = rounds * at_once;
   const int c = (lane >> 1) & (ranks - 1), lanes = 2 * ranks;
-  const uint32_t red_at = cluster_address(smem_addr(red), c);
+  const uint32_t red_at = cluster_addr(smem_addr(red), c);
   for (int j0 = 0; j0 * ranks + rank < slots; j0 += 32 / lanes) {
     const int slot = (j0 + lane / lanes) * ranks + rank, n = (slot * ctas + cta) * 16 + 8 * (lane & 1);
     const bool on = slot < slots && n < a.N;
@@ -494,7 +438,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), NT <= 2 ? 2 : 1) matvec_ker
       float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
       if (on)
         for (int k = 0; k < kw; ++k) {
-          const float4 u = ld_cluster(at + k * red_warp * 4), v = ld_cluster(at + k * red_warp * 4 + 16);
+          const float4 u = ld_cluster4(at + k * red_warp * 4), v = ld_cluster4(at + k * red_warp * 4 + 16);
           add8(sum, u, v);
         }
       for (int d = 2; d < lanes; d *= 2)
@@ -511,12 +455,12 @@ __global__ void __launch_bounds__(32 * warps_of(NT), NT <= 2 ? 2 : 1) matvec_ker
       }
     }
   }
-  cluster_barrier();  // the sums are read
+  cluster_sync();  // the sums are read
 }
 
 template <int NT, bool SCALED, int LAY>
 frt_status launch_one(Args a, cudaStream_t stream) {
-  constexpr int kPerSM = NT <= 2 ? 2 : 1, kWarps = warps_of(NT), kAhead = ahead_of(NT);
+  constexpr int kPerSM = ctas_of(NT), kWarps = warps_of(NT);
   a.tiles = (int)(((int64_t)a.N + 15) / 16);
   const int mr = NT == 1 && a.rows < 8 ? a.rows : 8;
   const int x_rows = NT == 1 ? mr : 8 * NT;
@@ -584,14 +528,18 @@ frt_status launch_layout(const Args& a, cudaStream_t stream) {
   return a.swizzled ? launch_one<NT, SCALED, 2>(a, stream) : launch_one<NT, SCALED, 1>(a, stream);
 }
 template <bool SCALED>
+frt_status launch_few(const Args& a, cudaStream_t stream) {
+  return a.rows <= 8 ? launch_layout<1, SCALED>(a, stream) : launch_layout<2, SCALED>(a, stream);
+}
+// Up to this many rows of x the warps' products carry them.
+constexpr int kFewRows = 16;
 frt_status launch_rows(Args a, cudaStream_t stream) {
-  for (a.m0 = 0; a.m0 < a.M; a.m0 += 64) {
-    a.rows = a.M - a.m0 < 64 ? a.M - a.m0 : 64;
-    const frt_status st = a.rows <= 8    ? launch_layout<1, SCALED>(a, stream)
-                          : a.rows <= 16 ? launch_layout<2, SCALED>(a, stream)
-                          : a.rows <= 32 ? launch_layout<4, SCALED>(a, stream)
-                          : a.rows <= 48 ? launch_layout<6, SCALED>(a, stream)
-                                         : launch_layout<8, SCALED>(a, stream);
+  for (a.m0 = 0; a.m0 < a.M; a.m0 += kTileXRows) {
+    a.rows = std::min(a.M - a.m0, kTileXRows);
+    const bool scaled = a.form == kXScaled16 || a.form == kXE4M3Block;
+    const frt_status st = a.rows > kFewRows ? launch_matvec_tiles(a, stream)
+                          : scaled          ? launch_few<true>(a, stream)
+                                            : launch_few<false>(a, stream);
     if (st != FRT_OK) return st;
   }
   return FRT_OK;
@@ -637,5 +585,5 @@ extern "C" frt_status frt_matvec_nvfp4(const void* x, const float* x_scales, con
     case FRT_X_E4M3_BLOCK: a.form = kXE4M3Block; break;
     default: a.form = kXNvfp4; break;
   }
-  return a.form == kXScaled16 || a.form == kXE4M3Block ? launch_rows<true>(a, stream) : launch_rows<false>(a, stream);
+  return launch_rows(a, stream);
 }
