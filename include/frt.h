@@ -444,7 +444,7 @@ frt_status frt_gate_residual_adarms_fp8(const void* x, const void* gate, const v
  *   Two rows of one call with the same slot leave it unspecified.
  *   16-bit pointers, cos_tab and sin_tab 16-byte aligned.
  *   Layout rule: Hq, Hkv > 0, Hq % Hkv == 0, hd > 0 and hd % 16 == 0,
- *   max_pos > 0, capacity > 0.  Unsupported: hd > 256.
+ *   max_pos > 0, capacity > 0.  Unsupported: hd > 256, M * Hq >= 2^31.
  *
  * frt_nvfp4_kvcache_read: rows of the cache back in 16 bits:
  *   k_out[i, g, :] = code * sf * gs of slot slots[i] (code * sf exact, one

@@ -45,9 +45,21 @@ struct WriteArgs {
   int max_pos, capacity;
   float eps, inv_hd;
   double inv_hd64;
-  bool narrow;                // (token, head) indices fit 32 bits
-  int64_t warps_q, warps_kv;  // warps that hold Q heads, and K (or V) heads
+  int q_units;                // units of kQHeads Q heads of a token
+  uint32_t q_mul, kv_mul;     // i / d = (i + umulhi(i, mul)) >> shift, 0 <= i < 2^31
+  int q_shift, kv_shift;
+  int64_t warps_q, warps_kv;  // warps that hold Q units, and K (or V) heads
 };
+constexpr int kQHeads = 2;
+
+__device__ __forceinline__ int divide(int i, uint32_t mul, int shift) {
+  return (int)((__umulhi((uint32_t)i, mul) + (uint32_t)i) >> shift);
+}
+void divisor(int d, uint32_t* mul, int* shift) {
+  *shift = 0;
+  while ((1LL << *shift) < d) ++*shift;
+  *mul = (uint32_t)((((1ULL << *shift) - d) << 32) / d + 1);
+}
 
 // Exact a * b - c * d of fp32 numbers as an unevaluated pair (to ~2^-48 of the
 // larger product).
@@ -82,81 +94,103 @@ __device__ __forceinline__ float amax8_or_inf(const float* y) {
 template <int DT, int P>
 __global__ void __launch_bounds__(kThreads, 4) write_kernel(WriteArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int kind = w < a.warps_q ? kQ : w < a.warps_q + a.warps_kv ? kK : kV;
-  const int64_t w0 = kind == kQ ? 0 : kind == kK ? a.warps_q : a.warps_q + a.warps_kv;
-  const int H = kind == kQ ? a.Hq : a.Hkv;
-  const int64_t item = (w - w0) * (32 / P) + lane / P;  // (token, head) of this lane group
-  const int l = lane % P;
+  // K's heads first, which take longest
+  int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  int kind = kK;
+  if (w >= a.warps_kv) {
+    w -= a.warps_kv;
+    kind = kV;
+    if (w >= a.warps_kv) {
+      w -= a.warps_kv;
+      kind = kQ;
+    }
+  }
+  const int64_t count = (int64_t)a.M * (kind == kQ ? a.q_units : a.Hkv);  // (below 2^31)
+  const int64_t item = w * (32 / P) + lane / P;                           // of this lane group
+  bool on = item < count && lane % P < a.L;
+  // Lanes without work load what the last one loads; nothing is stored for them.
+  const int l = min(lane % P, a.L - 1);
+  const int it = (int)min(item, count - 1);
+  const int i = kind == kQ ? divide(it, a.q_mul, a.q_shift) : divide(it, a.kv_mul, a.kv_shift);
+  const int h = kind == kQ ? (it - i * a.q_units) * kQHeads : it - i * a.Hkv;
   const int heads = a.Hq + 2 * a.Hkv;
-  bool on = l < a.L && item < (int64_t)a.M * H;
-  int64_t i = 0;
-  if (on) i = a.narrow ? (int64_t)((uint32_t)item / (uint32_t)H) : item / H;
-  const int h = on ? (int)(item - i * H) : 0;
   const int C = 2 * a.L;  // chunks of a head
 
-  // The loads that depend on nothing are issued together: positions (constant,
-  // before the wait) and qkv; the RoPE rows follow the position.
-  const bool there = on;
+  // constant inputs before the wait
   int p = 0, slot = 0;
-  if (on && FRT_IDX_OK(i, a.M)) {
+  if (FRT_IDX_OK(i, a.M)) {
     p = __ldg(a.positions + i);
     slot = a.slots != nullptr ? __ldg(a.slots + i) : p;
   }
   const uint4* norm_w = kind == kQ ? a.q_norm_w : a.k_norm_w;
   const bool normed = kind != kV && norm_w != nullptr;
   uint4 w_lo = make_uint4(0, 0, 0, 0), w_hi = w_lo;
-  if (on && normed && FRT_IDX_OK(l + a.L, C)) {
+  if (normed && FRT_IDX_OK(l + a.L, C)) {
     w_lo = __ldg(norm_w + l);
     w_hi = __ldg(norm_w + l + a.L);
   }
   const float gs = kind == kQ ? 1.0f : __ldg(a.kv_scales + (kind - kK));
   pdl_enter();
 
-  const int64_t in0 = (i * heads + (kind == kQ ? h : kind == kK ? a.Hq + h : a.Hq + a.Hkv + h)) * C + l;
-  uint4 x_lo = make_uint4(0, 0, 0, 0), x_hi = x_lo;
-  if (there && FRT_IDX_OK(in0 + a.L, (int64_t)a.M * heads * C)) {
+  // x of the head (of both heads of a Q unit): issued before the position is
+  // looked at, which the RoPE rows follow
+  const int64_t x_chunks = (int64_t)a.M * heads * C;
+  const int64_t in0 = (int64_t)i * heads * C + (kind == kQ ? h : kind == kK ? a.Hq + h : a.Hq + a.Hkv + h) * C + l;
+  const bool second = kind == kQ && h + 1 < a.Hq;
+  uint4 x_lo = make_uint4(0, 0, 0, 0), x_hi = x_lo, x2_lo = x_lo, x2_hi = x_lo;
+  if (FRT_IDX_OK(in0 + a.L, x_chunks)) {
     x_lo = ld_stream(a.qkv + in0);
     x_hi = ld_stream(a.qkv + in0 + a.L);
   }
-  if (on && (p < 0 || p >= a.max_pos || slot < 0 || slot >= a.capacity)) {
-    if (a.status != nullptr && l == 0) atomicOr(a.status, 1);
+  if (second && FRT_IDX_OK(in0 + C + a.L, x_chunks)) {
+    x2_lo = ld_stream(a.qkv + in0 + C);
+    x2_hi = ld_stream(a.qkv + in0 + C + a.L);
+  }
+  if (p < 0 || p >= a.max_pos || slot < 0 || slot >= a.capacity) {
+    if (a.status != nullptr && on && l == 0) atomicOr(a.status, 1);
     on = false;
+    p = 0;
   }
   float2 cs[4], sn[4], nsn[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) cs[e] = sn[e] = nsn[e] = make_float2(0.0f, 0.0f);
-  if (on && kind != kV && FRT_SPAN_OK((int64_t)p * C + 2 * l, 2, (int64_t)a.max_pos * C)) {
+  if (kind != kV && FRT_SPAN_OK((int64_t)p * C + 2 * l, 2, (int64_t)a.max_pos * C)) {
     const float* c = reinterpret_cast<const float*>(a.cos_tab + (int64_t)p * C + 2 * l);
     const float* s = reinterpret_cast<const float*>(a.sin_tab + (int64_t)p * C + 2 * l);
     load_rope_pairs<4>(c, s, cs, sn, nsn);
   }
-  float2 lo[4], hi[4];
-  unpack_pairs<DT, 4>(&x_lo.x, lo);
-  unpack_pairs<DT, 4>(&x_hi.x, hi);
 
   if (kind == kQ) {
-    if (normed) {
-      const float ss = group_sum<P>(sum_squares_pairs<4>(lo, hi));
-      const float r = head_rstd(ss, a.inv_hd, a.eps);
-      float2 wl[4], wh[4];
-      unpack_pairs<DT, 4>(&w_lo.x, wl);
-      unpack_pairs<DT, 4>(&w_hi.x, wh);
-      scale_pairs<4>(lo, r, wl);
-      scale_pairs<4>(hi, r, wh);
-    }
-    float2 o1[4], o2[4];
-    rope_pairs<4>(lo, hi, cs, sn, nsn, o1, o2);
-    uint4 s1, s2;
-    pack_pairs<DT, 4>(o1, &s1.x);
-    pack_pairs<DT, 4>(o2, &s2.x);
-    const int64_t q0 = (i * a.Hq + h) * C + l;
-    if (on && FRT_IDX_OK(q0 + a.L, (int64_t)a.M * a.Hq * C)) {
-      a.q_out[q0] = s1;
-      a.q_out[q0 + a.L] = s2;
+    const int64_t q0 = (int64_t)i * a.Hq * C + h * C + l;
+#pragma unroll
+    for (int n = 0; n < kQHeads; ++n) {
+      float2 lo[4], hi[4];
+      unpack_pairs<DT, 4>(n == 0 ? &x_lo.x : &x2_lo.x, lo);
+      unpack_pairs<DT, 4>(n == 0 ? &x_hi.x : &x2_hi.x, hi);
+      if (normed) {
+        const float ss = group_sum<P>(lane % P < a.L ? sum_squares_pairs<4>(lo, hi) : 0.0f);
+        const float r = head_rstd(ss, a.inv_hd, a.eps);
+        float2 wl[4], wh[4];
+        unpack_pairs<DT, 4>(&w_lo.x, wl);
+        unpack_pairs<DT, 4>(&w_hi.x, wh);
+        scale_pairs<4>(lo, r, wl);
+        scale_pairs<4>(hi, r, wh);
+      }
+      float2 o1[4], o2[4];
+      rope_pairs<4>(lo, hi, cs, sn, nsn, o1, o2);
+      uint4 s1, s2;
+      pack_pairs<DT, 4>(o1, &s1.x);
+      pack_pairs<DT, 4>(o2, &s2.x);
+      if (on && (n == 0 || second) && FRT_IDX_OK(q0 + n * C + a.L, (int64_t)a.M * a.Hq * C)) {
+        a.q_out[q0 + n * C] = s1;
+        a.q_out[q0 + n * C + a.L] = s2;
+      }
     }
     return;
   }
+  float2 lo[4], hi[4];
+  unpack_pairs<DT, 4>(&x_lo.x, lo);
+  unpack_pairs<DT, 4>(&x_hi.x, hi);
 
   // y of this lane's two 8-element units
   float y1[8], y2[8];
@@ -169,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(WriteArgs a) {
       for (int e = 0; e < 4; ++e)
         ss += ((double)(lo[e].x * lo[e].x) + (double)(lo[e].y * lo[e].y)) +
               ((double)(hi[e].x * hi[e].x) + (double)(hi[e].y * hi[e].y));
+      if (lane % P >= a.L) ss = 0.0;  // (a copy of another lane)
 #pragma unroll
       for (int o = P / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
       r = Split32(rsqrt_f64(fma(ss, a.inv_hd64, (double)a.eps)));
@@ -224,9 +259,10 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(WriteArgs a) {
   if (b2 == inf) sf2 = 0x7F, c2 = 0;
 
   const int t = kind - kK;
+  if (!on) return;
   const int64_t row = (int64_t)slot * a.Hkv + h;
   const int64_t quad = ((int64_t)(slot >> 2) * a.Hkv + h) * a.L;
-  if (on && FRT_IDX_OK(row * C + u2, (int64_t)a.capacity * a.Hkv * C)) {
+  if (FRT_IDX_OK(row * C + u2, (int64_t)a.capacity * a.Hkv * C)) {
     a.codes[t][row * C + u1] = c1;
     a.codes[t][row * C + u2] = c2;
     const int64_t sf_bytes = (int64_t)((a.capacity + 3) >> 2) * a.Hkv * a.L * 4;
@@ -241,10 +277,13 @@ frt_status launch_write(const WriteArgs& a0, cudaStream_t stream) {
   WriteArgs a = a0;
   const int P = a.L > 8 ? 16 : a.L > 4 ? 8 : a.L > 2 ? 4 : a.L;
   const int per = 32 / P;
-  a.narrow = (int64_t)a.M * a.Hq < 0x7FFFFFFF;
   a.inv_hd64 = 1.0 / (16 * a.L);
   a.inv_hd = (float)a.inv_hd64;
-  a.warps_q = ((int64_t)a.M * a.Hq + per - 1) / per;
+  a.q_units = (a.Hq + kQHeads - 1) / kQHeads;
+  divisor(a.q_units, &a.q_mul, &a.q_shift);
+  divisor(a.Hkv, &a.kv_mul, &a.kv_shift);
+  if ((int64_t)a.M * (a.Hq > a.Hkv ? a.Hq : a.Hkv) > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
+  a.warps_q = ((int64_t)a.M * a.q_units + per - 1) / per;
   a.warps_kv = ((int64_t)a.M * a.Hkv + per - 1) / per;
   const int64_t blocks = (a.warps_q + 2 * a.warps_kv + kWarps - 1) / kWarps;
   if (blocks > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
