@@ -436,7 +436,8 @@ frt_status frt_gate_residual_adarms_fp8(const void* x, const void* gate, const v
  *            where sf is 0),
  *   the decisions of the NVFP4 producers above.  A block that holds a NaN or
  *   an infinity gets the NaN scale factor 0x7F and zero codes.
- *   positions     device int32 [M], the RoPE positions.
+ *   positions     device int32 [M], the RoPE positions (not a constant input
+ *                 here: a kernel launched just before may write it).
  *   slots         device int32 [M], the cache slots; NULL: slot = position.
  *   status        as op (b), bit 0: a row whose position is outside
  *                 [0, max_pos) or whose slot is outside [0, capacity) is
@@ -509,7 +510,9 @@ frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8_t* k_sf, c
  *                 or a q_indptr that is out of order, outside [0, M] or gives a
  *                 sequence more than max_q_len tokens (the extra tokens are
  *                 left as they were); or a page outside [0, capacity /
- *                 page_size) (its positions are left out).
+ *                 page_size) (its positions are left out);  bit 1  a kernel for
+ *                 many query rows gave up a wait (see frt_set_wait_polls): what
+ *                 it wrote means nothing.
  *   NaN: a NaN scale factor in a position that a row sees makes that row NaN;
  *   whatever unseen positions hold has no effect.
  *   Layout rule: Hq, Hkv > 0, Hq % Hkv == 0, hd > 0 and hd % 16 == 0,
@@ -535,13 +538,15 @@ typedef enum { FRT_X_16BIT = 0, FRT_X_E4M3 = 1, FRT_X_E4M3_BLOCK = 2, FRT_X_NVFP
 
 /*
  * Matrix-vector products with NVFP4 weights, for the few rows of a decoding or
- * action step (any M is accepted; the kernel is built for M up to about 64):
+ * action step (any M is accepted; the weights are read once per 128 rows):
  *   y[i, n] = sum_k x[i, k] w[n, k] + bias[n],
  *   w[n, k] = e2m1 code * sf[n, k / 16] * w_scale,
  * x as the 16-bit type or as this library's FP8 / NVFP4 ops wrote it.  Products
  * are exact, sums fp32, one rounding to 16 bits.  (bf16 rows are carried as
  * fp16 times a power of two per row and 128 columns: exact down to 2^-28 of the
- * block's largest magnitude, and below that to 2^-39 of it.)
+ * block's largest magnitude, and below that to 2^-39 of it.)  A NaN scale factor
+ * of row n of w makes column n of y NaN.  No atomics: the same call gives the
+ * same bits.
  *
  *   x         device [M, K] 16-bit or e4m3 bytes, or [M, K/2] e2m1 bytes.
  *   x_scales  device fp32: 16BIT ignored; E4M3 [1]; E4M3_BLOCK [M,
@@ -592,7 +597,8 @@ frt_status frt_copy_rows(const void* src, void* dst, int rows, int row_bytes, cu
  * writes visible (griddepcontrol.wait), before it reads its data inputs (x,
  * residual, qkv, gate_up, the AdaRMSNorm condition rows) or writes anything.
  * Its constant inputs -- norm weights, RoPE tables, positions and the scale
- * inputs (static_scale, kv_scales, global_scale) -- are read before that
+ * inputs (static_scale, kv_scales, global_scale), and the matrix-vector
+ * product's weights -- may be read before that
  * wait, so they must not be written by the kernel launched just before it on
  * the same stream (no kernel of this library writes them; a host copy or a
  * kernel further back is fine: a kernel is scheduled early only once every
@@ -612,6 +618,10 @@ int frt_get_pdl(void);
  * default bound, whatever this setting) for the copies it issued to land, and
  * returns.  Only a failing device makes the default bound run out; a bound of
  * 0 gives up at once on every token, which lets a test check that path.
+ * The tensor-core kernels of frt_attn_nvfp4_kvcache (many query rows) and
+ * frt_matvec_nvfp4 (more than 16 rows) bound their waits for their own products
+ * in the same way; the first sets bit 1 of its status word, the second writes
+ * NaN.
  * Process-wide, read at each launch, like frt_set_pdl.
  * Returns FRT_ERR_INVALID_ARG for polls < 0.
  */

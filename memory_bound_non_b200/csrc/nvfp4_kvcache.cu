@@ -117,11 +117,6 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(WriteArgs a) {
   const int C = 2 * a.L;  // chunks of a head
 
   // constant inputs before the wait
-  int p = 0, slot = 0;
-  if (FRT_IDX_OK(i, a.M)) {
-    p = __ldg(a.positions + i);
-    slot = a.slots != nullptr ? __ldg(a.slots + i) : p;
-  }
   const uint4* norm_w = kind == kQ ? a.q_norm_w : a.k_norm_w;
   const bool normed = kind != kV && norm_w != nullptr;
   uint4 w_lo = make_uint4(0, 0, 0, 0), w_hi = w_lo;
@@ -132,6 +127,11 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(WriteArgs a) {
   const float gs = kind == kQ ? 1.0f : __ldg(a.kv_scales + (kind - kK));
   pdl_enter();
 
+  int p = 0, slot = 0;
+  if (FRT_IDX_OK(i, a.M)) {
+    p = __ldg(a.positions + i);
+    slot = a.slots != nullptr ? __ldg(a.slots + i) : p;
+  }
   // x of the head (of both heads of a Q unit): issued before the position is
   // looked at, which the RoPE rows follow
   const int64_t x_chunks = (int64_t)a.M * heads * C;
