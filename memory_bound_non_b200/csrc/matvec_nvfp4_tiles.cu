@@ -242,7 +242,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
         st_shared16(to + line0, make_uint4(v[0], v[1], v[2], v[3]));
         st_shared16(to + line1, make_uint4(v[4], v[5], v[6], v[7]));
       }
-      load_w(w[u]);
       k_left -= kGroup;
 #pragma unroll
       for (int n = 0; n < kXEach; ++n) {
@@ -252,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
         if (kScaled && l == 0) xs[u * NX + r] = x[n].scale * w_scale;
         x[n] = x_row[n].next(a, r < a.rows && k_left > 0);
       }
+      load_w(w[u]);  // (behind x, which is wanted sooner)
       fence_proxy_async_smem();
       tc_fence_before();
       __syncthreads();
