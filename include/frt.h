@@ -445,7 +445,8 @@ frt_status frt_gate_residual_adarms_fp8(const void* x, const void* gate, const v
  *   Two rows of one call with the same slot leave it unspecified.
  *   16-bit pointers, cos_tab and sin_tab 16-byte aligned.
  *   Layout rule: Hq, Hkv > 0, Hq % Hkv == 0, hd > 0 and hd % 16 == 0,
- *   max_pos > 0, capacity > 0.  Unsupported: hd > 256, M * Hq >= 2^31.
+ *   max_pos > 0, capacity > 0.  Unsupported: hd > 256, Hq > 2^20, M * Hq >=
+ *   2^31.
  *
  * frt_nvfp4_kvcache_read: rows of the cache back in 16 bits:
  *   k_out[i, g, :] = code * sf * gs of slot slots[i] (code * sf exact, one
@@ -455,7 +456,7 @@ frt_status frt_gate_residual_adarms_fp8(const void* x, const void* gate, const v
  *   status        bit 0: a slot outside [0, capacity); its rows stay as they
  *                 were.
  *   Layout rule: n >= 0, Hkv, capacity > 0, hd > 0 and hd % 16 == 0.
- *   Unsupported: hd > 256.
+ *   Unsupported: hd > 256, Hkv > 2^20.
  */
 frt_status frt_qkv_norm_rope_nvfp4_kvcache(const void* qkv, const void* q_norm_w, const void* k_norm_w,
                                            const float* cos_tab, const float* sin_tab, const int32_t* positions,
@@ -517,8 +518,8 @@ frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8_t* k_sf, c
  *   whatever unseen positions hold has no effect.
  *   Layout rule: Hq, Hkv > 0, Hq % Hkv == 0, hd > 0 and hd % 16 == 0,
  *   n_seqs > 0, capacity > 0, max_q_len > 0, max_kv_len >= 0, softmax_scale
- *   finite; n_seqs == 1 without q_indptr.  Unsupported: hd > 256, more than
- *   65535 sequences, max_kv_len > 2^31 - 256.
+ *   finite; n_seqs == 1 without q_indptr.  Unsupported: hd > 256, Hq > 2^20,
+ *   more than 65535 sequences, max_kv_len > 2^31 - 256.
  */
 size_t frt_attn_nvfp4_workspace_bytes(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len);
 frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_codes, const uint8_t* k_sf, const uint8_t* v_codes,

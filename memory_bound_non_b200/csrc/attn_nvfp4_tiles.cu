@@ -14,6 +14,10 @@
 //   P -> TMEM (binary16, over S), O += P V  (tcgen05, P from TMEM, O in TMEM)
 // Two CTAs share an SM (hd <= 192), so that one's products run beside the
 // other's conversions and exponentials; that is all the pipelining there is.
+// Measured, 512 tokens of 16/8 heads of 128 over 4608 positions: 47.5 us, 390
+// TFLOP/s (the warps' products took 142 us); a tile takes 3700 clocks of an SM
+// against the 1024 of its bound, in barriers and in the latency of what stands
+// between them; a call costs 10 us before and behind its tiles.
 //
 // Operand layouts: Q and K as rows of 64 dimensions (128 bytes) with the
 // 128-byte swizzle, k-major; V in the same form, which read as the B operand of

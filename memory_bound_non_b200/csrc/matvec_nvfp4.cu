@@ -2,7 +2,10 @@
 //
 // What bounds it: the weights, 0.5625 B each, read once; against that stand one
 // cvt and one multiply per two weights and one mma.m16n8k16 per 256 weights and
-// 8 rows.
+// 8 rows.  1 x 4096 -> 32768: 75.6 MB, 11.5 us at the copy rate, 19 us measured
+// (4.0 TB/s; a plain read of 67 MB by bulk copies takes 14.6 us, launch
+// included).  Small ones are bound by the launch and three dependent steps: 1 x
+// 1024 -> 2560 3.6 us.
 //
 // Mapping.  16 weight rows on the 16-row side of the mma, 8 NT rows of x on
 // the other.  The order of k inside a product is free: with g = lane / 4 and t

@@ -14,7 +14,11 @@
 // step (bf16, block-scaled FP8) the sums of a step go to one of two accumulators
 // and are added to registers with their factors while the next step runs.
 // With few tiles the CTAs of a cluster split k and join their sums through
-// distributed shared memory.
+// distributed shared memory.  Measured: 41 rows of 2048 (block-scaled FP8) to
+// 16384 18 us (3.1 us of bytes, 1.7 of products), 62 of 256 to 11682 5.0 us; a
+// step takes 1600 clocks, a chain of conversion, barrier and sums in which no
+// single part stands out (without x 16 % less, without the factors' sums 14 %,
+// without the products 2 %).
 #include <algorithm>
 
 #include "matvec_nvfp4.cuh"

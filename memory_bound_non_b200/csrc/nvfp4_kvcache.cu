@@ -3,14 +3,20 @@
 // Writer.  Per head of hd elements: RMSNorm, rotate-half RoPE, then for K and
 // V blocks of 16 with an e4m3 factor sf = e4m3(amax / (6 gs)) and codes
 // e2m1(y / (sf gs)) (scaled by rounded reciprocals, as the NVFP4 producers).
-// 2 B an element are read, 2 B of Q or 0.5625 B of K and V written: bound by
-// those bytes on large batches, by latency on small ones.
+// 2 B an element are read, 2 B of Q or 0.5625 B of K and V written.
 //
 // Mapping: hd/16 lanes hold a head, each 8 elements of the lower half and
 // their 8 rotation partners of the upper half (two 16-byte loads), so RoPE
 // needs no exchange, a block is two neighbouring 8-element units and the head
 // reduction is a few shuffles inside a group of P >= hd/16 lanes.  A warp
-// holds heads of one kind (Q, K or V) only.
+// holds heads of one kind (Q, K or V) only; of Q a lane group takes two heads
+// of a token, which share its RoPE rows.
+//
+// What bounds it: 4096 tokens of 32/8 heads of 128 take about 27 us, 2.1 times
+// their bytes at the copy rate: half the issue slots (K's exact products and the
+// 16-bit unpacking) and the wait for rows at random positions of the tables.
+// With one head to a lane group and 64-bit index arithmetic it took 39 us.  A
+// few tokens are bound by the launch (4.2 us with the reader, two launches).
 //
 // K decides its codes next to e2m1 borders, so y has to be the exact value
 // rounded once: products as exact pairs (p, e) by FMA, their difference by
@@ -299,14 +305,15 @@ frt_status launch_write(const WriteArgs& a0, cudaStream_t stream) {
 
 // Reader: bound by the 4 B an element pair it writes.  A thread takes kReadUnits
 // units of 8 codes (4 bytes to one 16-byte store) of K and of V, their loads
-// issued together.
+// issued together: 16384 slots of 8 heads of 128 in 17.0 us, 5.05 TB/s (26 us
+// with a unit of one tensor to a thread).
 constexpr int kReadUnits = 2;
 template <int DT>
 __global__ void __launch_bounds__(kThreads) read_kernel(const uint32_t* k_codes, const uint8_t* k_sf,
                                                         const uint32_t* v_codes, const uint8_t* v_sf,
                                                         const float* kv_scales, const int32_t* slots, uint4* k_out,
                                                         uint4* v_out, int32_t* status, int n, int Hkv, int L,
-                                                        int capacity) {
+                                                        int capacity, uint32_t u_mul, int u_shift) {
   const float gs[2] = {__ldg(kv_scales), __ldg(kv_scales + 1)};
   pdl_enter();
   const int U = 2 * L * Hkv;  // 8-element units of a slot
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const uint32_t* k_codes,
 #pragma unroll
   for (int j = 0; j < kReadUnits; ++j) {
     const int64_t at = at0 + j * kThreads;
-    const int64_t i = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)at / (uint32_t)U) : at / U;
+    const int64_t i = total <= 0x7FFFFFFF ? (int64_t)divide((int)at, u_mul, u_shift) : at / U;
     u[j] = (int)(at - i * U);
     slot[j] = -1;
     if (at < total && FRT_IDX_OK(i, n)) {
@@ -345,18 +352,20 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const uint32_t* k_codes,
     if (slot[j] < 0 || !FRT_IDX_OK(at, total)) continue;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const float sf = e4m3_value(f[j][t]);
+      const uint32_t sf = e4m3_to_both(f[j][t]);
       uint32_t h[4], o[4];
       e2m1x8_to_half2(w[j][t], h);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 v = Pack16<FRT_F16>::to_float2(h[e]);
-        o[e] = Pack16<DT>::from_float2((v.x * sf) * gs[t], (v.y * sf) * gs[t]);
+      for (int e = 0; e < 4; ++e) {  // code * sf is exact in binary16
+        const float2 v = __fmul2_rn(Pack16<FRT_F16>::to_float2(hmul2(h[e], sf)), make_float2(gs[t], gs[t]));
+        o[e] = Pack16<DT>::from_float2(v.x, v.y);
       }
       (t == 0 ? k_out : v_out)[at] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
+
+constexpr int kMaxHeads = 1 << 20;  // (head indices times hd stay within 32 bits)
 
 bool cache_ok(const void* k_codes, const void* k_sf, const void* v_codes, const void* v_sf, const void* kv_scales) {
   for (const void* p : {k_codes, k_sf, v_codes, v_sf})
@@ -379,7 +388,7 @@ extern "C" frt_status frt_qkv_norm_rope_nvfp4_kvcache(const void* qkv, const voi
   if (M < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || hd <= 0 || hd % 16 != 0 || max_pos <= 0 || capacity <= 0 ||
       !valid_dtype(dt))
     return FRT_ERR_INVALID_ARG;
-  if (hd > 256) return FRT_ERR_UNSUPPORTED;
+  if (hd > 256 || Hq > kMaxHeads) return FRT_ERR_UNSUPPORTED;
   if (M == 0) return FRT_OK;
   for (const void* p : {qkv, (const void*)cos_tab, (const void*)sin_tab, (const void*)q_out})
     if (p == nullptr || !aligned(p, 16)) return FRT_ERR_INVALID_ARG;
@@ -418,7 +427,7 @@ extern "C" frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8
                                              void* k_out, void* v_out, int32_t* status, int n, int Hkv, int hd,
                                              int capacity, frt_dtype dt, cudaStream_t stream) {
   if (n < 0 || Hkv <= 0 || hd <= 0 || hd % 16 != 0 || capacity <= 0 || !valid_dtype(dt)) return FRT_ERR_INVALID_ARG;
-  if (hd > 256) return FRT_ERR_UNSUPPORTED;
+  if (hd > 256 || Hkv > kMaxHeads) return FRT_ERR_UNSUPPORTED;
   if (n == 0) return FRT_OK;
   if (!cache_ok(k_codes, k_sf, v_codes, v_sf, kv_scales) || k_out == nullptr || v_out == nullptr ||
       !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(slots, 4) || !aligned(status, 4))
@@ -426,8 +435,11 @@ extern "C" frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8
   const int64_t blocks = ((int64_t)n * Hkv * (hd / 8) + kThreads * kReadUnits - 1) / (kThreads * kReadUnits);
   if (blocks > 0x7FFFFFFF) return FRT_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks), block(kThreads);
+  uint32_t u_mul;
+  int u_shift;
+  divisor(Hkv * (hd / 8), &u_mul, &u_shift);
   return launch(dt == FRT_F16 ? read_kernel<FRT_F16> : read_kernel<FRT_BF16>, grid, block, 0, stream,
                 reinterpret_cast<const uint32_t*>(k_codes), k_sf, reinterpret_cast<const uint32_t*>(v_codes), v_sf,
                 kv_scales, slots, static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), status, n, Hkv, hd / 16,
-                capacity);
+                capacity, u_mul, u_shift);
 }
