@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
   unsigned char* smem = raw_smem + (base - smem_addr(raw_smem));
   float* xs = reinterpret_cast<float*>(smem + 2 * T::kStage);  // [3][NX]
   uint64_t* bar = reinterpret_cast<uint64_t*>(xs + 3 * NX);    // [2]
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 2);
+  uint64_t* drained = bar + 2;  // the products behind a wait that ran out
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bar + 3);
   int* gave_up_at = reinterpret_cast<int*>(tmem_at + 1);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
   if (threadIdx.x == 0) {
     mbar_init(&bar[0], 1);
     mbar_init(&bar[1], 1);
+    mbar_init(drained, 1);
     mbar_init_fence();
     *gave_up_at = 0;
   }
@@ -287,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
   __syncthreads();
   if (*gave_up_at != 0) {  // a wait that ran out: the rows become NaN; the products end before TMEM is freed
     if (threadIdx.x == 0) {
-      tc_commit(&bar[steps & 1]);
-      for (int n = 0; n < 4; ++n) (void)mbar_wait_bounded(&bar[steps & 1], n & 1, 1 << 14);
+      tc_commit(drained);
+      (void)mbar_wait_bounded(drained, 0, 1 << 14);
     }
     __syncthreads();
 #pragma unroll

@@ -645,6 +645,20 @@ def test_matvec_nan_and_bits():
     assert torch.isnan(again[2]).all() and torch.equal(again[[0, 1, 3]], y[[0, 1, 3]])
 
 
+@pytest.mark.parametrize("dt,k", [("bf16", 144), ("f16", 512), ("f16", 4096)])
+def test_matvec_wait_that_runs_out(dt, k):
+    """With no polls allowed the kernel of many rows gives its waits up, writes NaN and ends; the next call is right."""
+    prev = frt.frt_get_wait_polls()
+    try:
+        frt.frt_set_wait_polls(0)
+        y, _, _ = matvec_case(40, 300, k, "16", dt=dt)
+        torch.cuda.synchronize()
+    finally:
+        frt.frt_set_wait_polls(prev)
+    assert torch.isnan(y).all()
+    check_matvec(40, 300, k, "16", dt=dt)
+
+
 # ------------------------------------------------------------ binding, all --
 def test_binding_refusals():
     c = Case([1], [50], 4, 2, 64)
