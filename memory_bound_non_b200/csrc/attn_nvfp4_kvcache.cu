@@ -38,7 +38,6 @@ namespace frt {
 namespace {
 
 constexpr int kTile = 32;  // slots
-constexpr int kSMs = 148;
 using Args = AttnArgs;
 
 __device__ __forceinline__ uint32_t select_bits(uint32_t mask, uint32_t a, uint32_t b) {
@@ -759,10 +758,11 @@ Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_le
   const int64_t least = p.nt == 0 ? 1 : attn_warps(build, p.nt);  // tiles
   // CTAs that run at once; a batch of sequences, whose lengths differ, gets
   // four times as many
-  const int64_t want = (int64_t)kSMs * (p.nt == 0 ? (hd > 192 ? 1 : 2) : 16 / attn_warps(build, p.nt)) * (n_seqs > 1 ? 4 : 1);
+  const int per_sm = p.nt == 0 ? (hd > 192 ? 1 : 2) : 16 / attn_warps(build, p.nt), times = n_seqs > 1 ? 4 : 1;
+  const int64_t want = (int64_t)kSMs * per_sm * times;
   p.cluster = 0;
   p.chunks = 1;
-  while (p.chunks < 8 && ctas * p.chunks * 2 <= want && tiles > p.chunks * least) p.chunks *= 2;
+  while (p.chunks < 8 && ctas <= (int64_t)cluster_room(per_sm, 2 * p.chunks) * times && tiles > p.chunks * least) p.chunks *= 2;
   p.chunk_tiles = (int)tiles;
   if (p.chunks == 1) return p;
   // More chunks than a cluster has CTAs cost a second kernel and a way through

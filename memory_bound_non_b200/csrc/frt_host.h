@@ -52,6 +52,13 @@ inline frt_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t
   return launch_status();
 }
 
+constexpr int kSMs = 148;
+// Clusters of `ranks` CTAs (1, 2, 4 or 8) that the GPU holds at once, per_sm (1, 2
+// or 4) to an SM.  A cluster lies inside one GPC and the GPCs' SMs are no
+// multiple of 4 or 8: 33 of 4 and 15 of 8 where 148 SMs would hold 37 and 18.  A
+// grid cut for the latter runs a second wave, twice the time.
+int cluster_room(int per_sm, int ranks);
+
 // As launch(), with the grid grouped into thread-block clusters of
 // `cluster_x` CTAs along x (co-scheduled; they share distributed shared memory).
 template <typename... KArgs, typename... Args>

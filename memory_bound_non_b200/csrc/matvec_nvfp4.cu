@@ -30,7 +30,6 @@
 namespace frt {
 namespace {
 
-constexpr int kSMs = 148;
 constexpr int kAhead = 4;  // groups a warp has on their way
 // CTAs that share an SM and their warps: up to 8 rows of x two, above one of
 // twice the warps, which lays its many rows out once.
@@ -234,7 +233,7 @@ __host__ __device__ constexpr int sum_floats(int nt, int mr) { return (nt == 1 ?
 // SCALED: x has a factor per row and group.
 template <int NT, bool SCALED, int LAY>
 __global__ void __launch_bounds__(32 * warps_of(NT), ctas_of(NT)) matvec_kernel(const Args a) {
-  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps;
+  constexpr int kWarps = warps_of(NT);
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -484,7 +483,7 @@ frt_status launch_one(Args a, cudaStream_t stream) {
     const int k_groups = (a.groups + ranks - 1) / ranks;
     for (int kw = 1, log2 = 0; kw <= kWarps && kw <= k_groups; kw *= 2, ++log2) {
       for (int sm = kPerSM; sm >= 1; --sm) {
-        const int64_t ctas = kSMs * sm / ranks;
+        const int64_t ctas = cluster_room(sm, ranks);
         const int64_t used = a.tiles < ctas ? a.tiles : ctas;
         const int64_t per_round = used * (kWarps / kw);
         const int64_t rounds = (a.tiles + per_round - 1) / per_round;
@@ -520,7 +519,7 @@ frt_status launch_one(Args a, cudaStream_t stream) {
   static std::atomic<int> opted{48 * 1024};
   const frt_status st = opt_in_smem(matvec_kernel<NT, SCALED, LAY>, smem, opted);
   if (st != FRT_OK) return st;
-  const int ctas = kSMs * per_sm / a.cluster;
+  const int ctas = cluster_room(per_sm, a.cluster);
   const dim3 grid((unsigned)((a.tiles < ctas ? a.tiles : ctas) * a.cluster)), block(32 * kWarps);
   if (a.cluster > 1) return launch_cluster(matvec_kernel<NT, SCALED, LAY>, grid, block, smem, stream, a.cluster, a);
   return launch(matvec_kernel<NT, SCALED, LAY>, grid, block, smem, stream, a);
@@ -534,7 +533,9 @@ template <bool SCALED>
 frt_status launch_few(const Args& a, cudaStream_t stream) {
   return a.rows <= 8 ? launch_layout<1, SCALED>(a, stream) : launch_layout<2, SCALED>(a, stream);
 }
-// Up to this many rows of x the warps' products carry them.
+// The warps' products carry 16 rows of x at most.  There they still win: 16 rows
+// of 4096 to 32768 23.5-32 us against the tiles' 53-64, of 8192 to 8192 16-19
+// against 28-33, of 4096 to 1024 6.4-8.2 against 7.4-7.5 (the forms of x).
 constexpr int kFewRows = 16;
 frt_status launch_rows(Args a, cudaStream_t stream) {
   for (a.m0 = 0; a.m0 < a.M; a.m0 += kTileXRows) {

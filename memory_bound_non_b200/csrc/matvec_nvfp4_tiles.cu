@@ -30,7 +30,6 @@ constexpr int kThreads = 512;
 constexpr int kRows = 128;              // weight rows
 constexpr int kRegionA = kRows * 128;   // bytes of 64 k
 constexpr int kAhead = 3;
-constexpr int kSMs = 148;
 
 // NX: rows of x that the build carries (32, 64 or 128).
 template <int NX>
@@ -345,7 +344,7 @@ frt_status launch_tiles(MatvecArgs a, cudaStream_t stream) {
   a.tiles = (int)(((int64_t)a.N + kRows - 1) / kRows);
   // k is split while that fills the SMs better and leaves a CTA two steps
   a.cluster = 1;
-  while (a.cluster < 8 && a.tiles * a.cluster * 2 <= kSMs && a.groups >= 4 * a.cluster) a.cluster *= 2;
+  while (a.cluster < 8 && a.tiles <= cluster_room(1, 2 * a.cluster) && a.groups >= 4 * a.cluster) a.cluster *= 2;
   const dim3 grid((unsigned)(a.tiles * a.cluster)), block(kThreads);
   if (a.cluster > 1)
     return launch_cluster(tiles_kernel<NX, FORM>, grid, block, Tile<NX>::kSmem, stream, a.cluster, a, wait_polls());
