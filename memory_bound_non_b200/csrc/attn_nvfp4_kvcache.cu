@@ -30,6 +30,7 @@
 // than 4, so 2^11 <= p <= 2^15 for the largest and weights down to 2^-25 of it
 // are normal numbers.  The sum is taken of the rounded weights (a row of ones
 // beside V).  bf16 queries enter as binary16 times a power of two per row.
+#include <algorithm>
 #include <cmath>
 
 #include "attn_nvfp4.cuh"
@@ -756,19 +757,32 @@ Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_le
   // a CTA's smallest share: a tile for every warp
   const int build = hd <= 64 ? 64 : hd <= 128 ? 128 : hd <= 192 ? 192 : 256;
   const int64_t least = p.nt == 0 ? 1 : attn_warps(build, p.nt);  // tiles
-  // CTAs that run at once; a batch of sequences, whose lengths differ, gets
-  // four times as many
-  const int per_sm = p.nt == 0 ? (hd > 192 ? 1 : 2) : 16 / attn_warps(build, p.nt), times = n_seqs > 1 ? 4 : 1;
-  const int64_t want = (int64_t)kSMs * per_sm * times;
+  const int per_sm = p.nt == 0 ? (hd > 192 ? 1 : 2) : 16 / attn_warps(build, p.nt);
+  // The keys among the CTAs of a cluster: the cheapest of 1, 2, 4 and 8, in turns
+  // of a CTA (a tile for each warp) on a full SM.  A CTA costs about 2.5 besides
+  // its turns (measured: 5.5 to 7 us beside turns of 2.4 at hd 128, 4.3 beside 1.6
+  // at hd 64), CTAs beyond those that run at once come one wave after the other,
+  // a GPU that is not full is up to 0.6 faster, and the last wave ends unevenly.
+  // 33 sequences of 1500 keys and 8 heads take 22, 29, 41 and 64 us in 1, 2, 4
+  // and 8 parts, 64 of 8000 144, 139, 169 and 228.
   p.cluster = 0;
   p.chunks = 1;
-  while (p.chunks < 8 && ctas <= (int64_t)cluster_room(per_sm, 2 * p.chunks) * times && tiles > p.chunks * least) p.chunks *= 2;
+  double best = 0;
+  for (int c = 1; c <= 8 && (c == 1 || tiles > c / 2 * least); c *= 2) {
+    const double waves = (double)ctas / cluster_room(per_sm, c);
+    const double turns = (double)((tiles + c * least - 1) / (c * least));
+    const double cost = 2.5 * std::max(1.0, waves) + turns * std::max(0.6, waves) + (waves > 1 ? 0.3 * turns : 0.0);
+    if (c > 1 && cost >= best) continue;
+    best = cost;
+    p.chunks = c;
+  }
   p.chunk_tiles = (int)tiles;
   if (p.chunks == 1) return p;
   // More chunks than a cluster has CTAs cost a second kernel and a way through
-  // memory, about as long as kJoinRounds tiles of a warp (or CTA) take.
+  // memory, about as long as kJoinRounds tiles of a warp (or CTA) take.  Sequences
+  // whose lengths differ get twice as many CTAs as run at once.
   constexpr int64_t kJoinRounds = 8;
-  const int64_t most = want / ctas;
+  const int64_t most = std::max<int64_t>(1, (int64_t)kSMs * per_sm * (n_seqs > 1 ? 2 : 1) / ctas);
   int64_t per = (tiles + most - 1) / most;
   per = (per + least - 1) / least * least;
   if (tiles / (p.chunks * least) > per / least + kJoinRounds) {
