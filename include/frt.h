@@ -563,6 +563,7 @@ typedef enum { FRT_X_16BIT = 0, FRT_X_E4M3 = 1, FRT_X_E4M3_BLOCK = 2, FRT_X_NVFP
  *   x, w_codes, x_sf and w_sf 16-byte aligned; bias and y 2-byte, x_scales and
  *   w_scale 4-byte.
  *   Layout rule: N > 0, K > 0 and K % 16 == 0.  M == 0 does nothing.
+ *   Unsupported: N or K > 2^31 - 65536.
  */
 frt_status frt_matvec_nvfp4(const void* x, const float* x_scales, const uint8_t* x_sf, const uint8_t* w_codes,
                             const uint8_t* w_sf, const float* w_scale, const void* bias, void* y, int M, int N, int K,

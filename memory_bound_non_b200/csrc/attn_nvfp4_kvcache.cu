@@ -741,7 +741,8 @@ struct Plan {
 // 10 us and does 1 M such pairs in a microsecond, the kernel for few rows 5 us
 // and 0.27 M.
 constexpr int64_t kManyRows = 48, kManyPairs = 2500000;
-Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
+// for_workspace: whether and how a second kernel joins the chunks, no more.
+Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len, bool for_workspace) {
   Plan p;
   const int64_t rows = (int64_t)max_q_len * (Hq / Hkv);
   const double pairs = (double)rows * Hkv * n_seqs * max_kv_len * hd / 128;
@@ -758,6 +759,28 @@ Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_le
   const int build = hd <= 64 ? 64 : hd <= 128 ? 128 : hd <= 192 ? 192 : 256;
   const int64_t least = p.nt == 0 ? 1 : attn_warps(build, p.nt);  // tiles
   const int per_sm = p.nt == 0 ? (hd > 192 ? 1 : 2) : 16 / attn_warps(build, p.nt);
+  p.cluster = 0;
+  p.chunks = 1;
+  p.chunk_tiles = (int)tiles;
+  // More chunks than a cluster has CTAs cost a second kernel and a way through
+  // memory, about as long as kJoinRounds tiles of a warp (or CTA) take.  Sequences
+  // whose lengths differ get twice as many CTAs as run at once.  (By sizes alone:
+  // the caller asks for the workspace before the call, and perhaps without a GPU.)
+  constexpr int64_t kJoinRounds = 8;
+  const int64_t at_once = (int64_t)kSMs * per_sm;
+  int64_t in_cluster = 1;
+  while (in_cluster < 8 && ctas * in_cluster * 2 <= at_once) in_cluster *= 2;
+  if (in_cluster > 1) {
+    const int64_t most = at_once * (n_seqs > 1 ? 2 : 1) / ctas;
+    int64_t per = (tiles + most - 1) / most;
+    per = (per + least - 1) / least * least;
+    if (tiles / (in_cluster * least) > per / least + kJoinRounds) {
+      p.chunk_tiles = (int)per;
+      p.chunks = (int)((tiles + per - 1) / per);
+      return p;
+    }
+  }
+  if (for_workspace) return p;
   // The keys among the CTAs of a cluster: the cheapest of 1, 2, 4 and 8, in turns
   // of a CTA (a tile for each warp) on a full SM.  A CTA costs about 2.5 besides
   // its turns (measured: 5.5 to 7 us beside turns of 2.4 at hd 128, 4.3 beside 1.6
@@ -765,8 +788,6 @@ Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_le
   // a GPU that is not full is up to 0.6 faster, and the last wave ends unevenly.
   // 33 sequences of 1500 keys and 8 heads take 22, 29, 41 and 64 us in 1, 2, 4
   // and 8 parts, 64 of 8000 144, 139, 169 and 228.
-  p.cluster = 0;
-  p.chunks = 1;
   double best = 0;
   for (int c = 1; c <= 8 && (c == 1 || tiles > c / 2 * least); c *= 2) {
     const double waves = (double)ctas / cluster_room(per_sm, c);
@@ -775,21 +796,7 @@ Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_le
     if (c > 1 && cost >= best) continue;
     best = cost;
     p.chunks = c;
-  }
-  p.chunk_tiles = (int)tiles;
-  if (p.chunks == 1) return p;
-  // More chunks than a cluster has CTAs cost a second kernel and a way through
-  // memory, about as long as kJoinRounds tiles of a warp (or CTA) take.  Sequences
-  // whose lengths differ get twice as many CTAs as run at once.
-  constexpr int64_t kJoinRounds = 8;
-  const int64_t most = std::max<int64_t>(1, (int64_t)kSMs * per_sm * (n_seqs > 1 ? 2 : 1) / ctas);
-  int64_t per = (tiles + most - 1) / most;
-  per = (per + least - 1) / least * least;
-  if (tiles / (p.chunks * least) > per / least + kJoinRounds) {
-    p.chunk_tiles = (int)per;
-    p.chunks = (int)((tiles + per - 1) / per);
-  } else {
-    p.cluster = 1;
+    p.cluster = c > 1;
   }
   return p;
 }
@@ -839,8 +846,8 @@ using namespace frt;
 extern "C" size_t frt_attn_nvfp4_workspace_bytes(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len,
                                                  int max_kv_len) {
   if (!plan_args_ok(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len)) return 0;
-  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
-  if (p.chunks == 1 || p.cluster) return 0;
+  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len, true);
+  if (p.chunks == 1) return 0;
   return (size_t)M * Hq * (p.chunks * (8 + 4 * (size_t)hd) + 4);
 }
 
@@ -868,7 +875,7 @@ extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_cod
   const size_t need = frt_attn_nvfp4_workspace_bytes(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
     return FRT_ERR_INVALID_ARG;
-  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
+  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len, false);
   Args a = {};
   a.q = q;
   a.k_codes = k_codes;

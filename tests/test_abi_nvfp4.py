@@ -86,7 +86,7 @@ def matvec_call(M=4, N=64, K=128, x=A, xs=None, xsf=None, w=A, wsf=A, ws=A, bias
     (dict(wsf=None), INV), (dict(wsf=A + 4), INV), (dict(ws=None), INV), (dict(ws=A + 2), INV), (dict(y=None), INV),
     (dict(y=A + 1), INV), (dict(bias=A + 1), INV), (dict(xfmt=1), INV), (dict(xfmt=2), INV), (dict(xfmt=2, xs=A + 2), INV),
     (dict(xfmt=3, xs=A), INV), (dict(xfmt=3, xs=A, xsf=A + 8), INV), (dict(M=0), OK), (dict(M=0, x=None, y=None), OK),
-    (dict(M=0, K=8), INV),
+    (dict(M=0, K=8), INV), (dict(N=2**31 - 1), UNSUP), (dict(K=2**31 - 16), UNSUP),
 ])
 def test_matvec_host_validation(kw, want):
     assert matvec_call(**kw) == want
