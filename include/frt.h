@@ -621,7 +621,7 @@ int frt_get_pdl(void);
  * returns.  Only a failing device makes the default bound run out; a bound of
  * 0 gives up at once on every token, which lets a test check that path.
  * The tensor-core kernels of frt_attn_nvfp4_kvcache (many query rows) and
- * frt_matvec_nvfp4 (more than 16 rows) bound their waits for their own products
+ * frt_matvec_nvfp4 (more than 16 rows of x) bound their waits for their own products
  * in the same way; the first sets bit 1 of its status word, the second writes
  * NaN.
  * Process-wide, read at each launch, like frt_set_pdl.

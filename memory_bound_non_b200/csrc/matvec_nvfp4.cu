@@ -30,9 +30,11 @@
 namespace frt {
 namespace {
 
-constexpr int kAhead = 4;  // groups a warp has on their way
-// CTAs that share an SM and their warps: up to 8 rows of x two, above one of
-// twice the warps, which lays its many rows out once.
+// groups a warp has on their way (with the sums of 32 rows no registers are left
+// for more than two)
+__host__ __device__ constexpr int ahead_of(int nt) { return nt == 4 ? 2 : 4; }
+// CTAs that share an SM and their warps: up to 8 rows of x (NT 1) two, above (NT
+// 2 and 4) one of twice the warps, which lays its many rows out once.
 __host__ __device__ constexpr int ctas_of(int nt) { return nt == 1 ? 2 : 1; }
 __host__ __device__ constexpr int warps_of(int nt) { return 16 / ctas_of(nt); }
 
@@ -233,7 +235,7 @@ __host__ __device__ constexpr int sum_floats(int nt, int mr) { return (nt == 1 ?
 // SCALED: x has a factor per row and group.
 template <int NT, bool SCALED, int LAY>
 __global__ void __launch_bounds__(32 * warps_of(NT), ctas_of(NT)) matvec_kernel(const Args a) {
-  constexpr int kWarps = warps_of(NT);
+  constexpr int kWarps = warps_of(NT), kAhead = ahead_of(NT);
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), ctas_of(NT)) matvec_kernel(
 
 template <int NT, bool SCALED, int LAY>
 frt_status launch_one(Args a, cudaStream_t stream) {
-  constexpr int kPerSM = ctas_of(NT), kWarps = warps_of(NT);
+  constexpr int kPerSM = ctas_of(NT), kWarps = warps_of(NT), kAhead = ahead_of(NT);
   a.tiles = (int)(((int64_t)a.N + 15) / 16);
   const int mr = NT == 1 && a.rows < 8 ? a.rows : 8;
   const int x_rows = NT == 1 ? mr : 8 * NT;
@@ -531,20 +533,29 @@ frt_status launch_layout(const Args& a, cudaStream_t stream) {
 }
 template <bool SCALED>
 frt_status launch_few(const Args& a, cudaStream_t stream) {
-  return a.rows <= 8 ? launch_layout<1, SCALED>(a, stream) : launch_layout<2, SCALED>(a, stream);
+  return a.rows <= 8    ? launch_layout<1, SCALED>(a, stream)
+         : a.rows <= 16 ? launch_layout<2, SCALED>(a, stream)
+                        : launch_layout<4, SCALED>(a, stream);
 }
-// The warps' products carry 16 rows of x at most.  There they still win: 16 rows
-// of 4096 to 32768 23.5-32 us against the tiles' 53-64, of 8192 to 8192 16-19
-// against 28-33, of 4096 to 1024 6.4-8.2 against 7.4-7.5 (the forms of x).
-constexpr int kFewRows = 16;
+// Up to kFewRows rows of x the warps' products win: 16 rows of 4096 to 32768
+// 23.5-32 us against the tiles' 53-64, of 8192 to 8192 16-19 against 28-33, of
+// 4096 to 1024 6.4-8.2 against 7.4-7.5 (the forms of x).  Up to kMoreRows, which is
+// what they carry at most, they win where the weights are many: 32 rows of 4096
+// to 32768 35-46 against 54-65, of 2048 to 16384 13-15.4 against 15-16.8, of 4096
+// to 4096 11.1-11.9 against 10.9-11.3, of 256 to 11682 4.6-5.0 against 3.9-4.0.
+constexpr int kFewRows = 16, kMoreRows = 32;
+constexpr int64_t kManyWeights = 1 << 24;
+bool warps_win(const Args& a) {
+  return a.rows <= kFewRows || (a.rows <= kMoreRows && (int64_t)a.N * a.K >= kManyWeights);
+}
 constexpr int kMaxSize = 0x7FFF0000;  // (32-bit indices reach past N and K by less than 65536)
 frt_status launch_rows(Args a, cudaStream_t stream) {
   for (a.m0 = 0; a.m0 < a.M; a.m0 += kTileXRows) {
     a.rows = std::min(a.M - a.m0, kTileXRows);
     const bool scaled = a.form == kXScaled16 || a.form == kXE4M3Block;
-    const frt_status st = a.rows > kFewRows ? launch_matvec_tiles(a, stream)
-                          : scaled          ? launch_few<true>(a, stream)
-                                            : launch_few<false>(a, stream);
+    const frt_status st = !warps_win(a) ? launch_matvec_tiles(a, stream)
+                          : scaled      ? launch_few<true>(a, stream)
+                                        : launch_few<false>(a, stream);
     if (st != FRT_OK) return st;
   }
   return FRT_OK;

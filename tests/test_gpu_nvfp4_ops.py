@@ -609,6 +609,13 @@ def test_matvec_deep(m, n, k, fmt):
     check_matvec(m, n, k, fmt, seed=m)
 
 
+@pytest.mark.parametrize("fmt", ["16", "e4m3", "e4m3_block", "nvfp4"])
+@pytest.mark.parametrize("m,n,k,layout", [(17, 8200, 2064, "rows"), (24, 4100, 4128, "swizzled"), (32, 37500, 448, "rows"),
+                                          (25, 1030, 16384, "swizzled"), (150, 8192, 2048, "rows")])
+def test_matvec_many_weights(fmt, m, n, k, layout):
+    check_matvec(m, n, k, fmt, dt="f16" if m == 24 else "bf16", layout=layout, bias=m == 32, seed=m)
+
+
 @pytest.mark.parametrize("off", [1, 2, 4])
 def test_matvec_unaligned_output(off):
     check_matvec(3, 64, 128, "16", off=off, bias=True)
@@ -817,6 +824,7 @@ def test_in_bounds():
         return [matvec_case(m, n, k, f, layout=lay, bias=True, seed=m)[0]
                 for m, n, k, f, lay in ((1, 100, 144, "16", "rows"), (9, 33, 1040, "nvfp4", "swizzled"),
                                         (41, 300, 272, "e4m3_block", "swizzled"), (64, 17, 8192, "16", "rows"),
-                                        (10, 1024, 4096, "e4m3", "rows"), (130, 50, 48, "16", "swizzled"))]
+                                        (10, 1024, 4096, "e4m3", "rows"), (130, 50, 48, "16", "swizzled"),
+                                        (20, 8210, 2064, "e4m3", "rows"), (32, 4100, 4128, "16", "swizzled"))]
     for fn in (attn, cache, matvec):
         both_builds(fn)
