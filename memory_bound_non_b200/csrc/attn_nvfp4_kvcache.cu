@@ -817,7 +817,7 @@ bool plan_args_ok(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int
 template <int HD, bool EXACT, int NT>
 frt_status launch_attn(const Args& a, cudaStream_t stream) {
   using A = Attn<HD, EXACT, NT>;
-  static std::atomic<int> opted{48 * 1024};
+  static SmemOptIn opted;
   const frt_status st = opt_in_smem(attn_kernel<HD, EXACT, NT>, A::kSmem, opted);
   if (st != FRT_OK) return st;
   const dim3 grid((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), block(A::kThreads);

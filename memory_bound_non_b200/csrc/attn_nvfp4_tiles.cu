@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
 
 template <int HD>
 frt_status launch_tiles(const AttnArgs& a, cudaStream_t stream) {
-  static std::atomic<int> opted{48 * 1024};
+  static SmemOptIn opted;
   const frt_status st = opt_in_smem(tiles_kernel<HD>, Tile<HD>::kSmem, opted);
   if (st != FRT_OK) return st;
   const dim3 grid((unsigned)(a.Hkv * a.row_tiles * a.chunks), a.n_seqs), block(kThreads);

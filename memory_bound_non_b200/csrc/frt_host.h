@@ -4,6 +4,8 @@
 #include <cstdint>
 
 #include <atomic>
+#include <thread>
+
 #include <cuda_runtime.h>
 
 #include <cuda_runtime_api.h>
@@ -97,20 +99,36 @@ inline bool quant_args_ok(frt_quant qm, const float* static_scale, const float* 
   return block_scales != nullptr && aligned(block_scales, 4);
 }
 
-// Raises a kernel's dynamic shared memory limit to `bytes` once (the largest
-// size seen so far is kept in `opted`); needed above the 48 KB default.
+// Raises a kernel's dynamic shared memory limit on the current device to `bytes`
+// (needed above the 48 KB default); `opted` keeps the largest size that each
+// device has seen.  The limit is set under a lock, so that a thread with a
+// smaller size never lowers it behind one with a larger.
+struct SmemOptIn {
+  static constexpr int kDevices = 64;
+  std::atomic<int> bytes[kDevices] = {};
+  std::atomic_flag busy = ATOMIC_FLAG_INIT;
+};
 template <typename Kern>
-frt_status opt_in_smem(Kern kern, size_t bytes, std::atomic<int>& opted) {
-  if ((int)bytes > opted.load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
+frt_status opt_in_smem(Kern kern, size_t bytes, SmemOptIn& opted) {
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device >= SmemOptIn::kDevices) {
+    (void)cudaGetLastError();
+    return FRT_ERR_CUDA;
+  }
+  std::atomic<int>& seen = opted.bytes[device];
+  if ((int)bytes <= seen.load(std::memory_order_acquire)) return FRT_OK;
+  while (opted.busy.test_and_set(std::memory_order_acquire)) std::this_thread::yield();
+  frt_status st = FRT_OK;
+  if ((int)bytes > seen.load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess) {
+      seen.store((int)bytes, std::memory_order_release);
+    } else {
       (void)cudaGetLastError();
-      return FRT_ERR_CUDA;
-    }
-    int cur = opted.load(std::memory_order_relaxed);
-    while ((int)bytes > cur && !opted.compare_exchange_weak(cur, (int)bytes)) {
+      st = FRT_ERR_CUDA;
     }
   }
-  return FRT_OK;
+  opted.busy.clear(std::memory_order_release);
+  return st;
 }
 
 // Validation shared by the NVFP4 producers: scale-factor layout, the global

@@ -518,7 +518,7 @@ frt_status launch_one(Args a, cudaStream_t stream) {
     }
   }
   if (a.cluster == 0) return FRT_ERR_UNSUPPORTED;  // (never: a segment of one set always fits)
-  static std::atomic<int> opted{48 * 1024};
+  static SmemOptIn opted;
   const frt_status st = opt_in_smem(matvec_kernel<NT, SCALED, LAY>, smem, opted);
   if (st != FRT_OK) return st;
   const int ctas = cluster_room(per_sm, a.cluster);

@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
 
 template <int NX, XForm FORM>
 frt_status launch_tiles(MatvecArgs a, cudaStream_t stream) {
-  static std::atomic<int> opted{48 * 1024};
+  static SmemOptIn opted;
   const frt_status st = opt_in_smem(tiles_kernel<NX, FORM>, Tile<NX>::kSmem, opted);
   if (st != FRT_OK) return st;
   a.tiles = (int)(((int64_t)a.N + kRows - 1) / kRows);

@@ -4,6 +4,7 @@ lengths from none to long, odd sizes, masks that leave rows empty, pages,
 factors that are NaN in unseen places, streams, captured graphs, and a run of
 the operators together."""
 import math
+import threading
 
 import pytest
 import torch
@@ -650,6 +651,24 @@ def test_matvec_nan_and_bits():
     xn[2, 9] = float("nan")
     frt.frt_matvec_nvfp4(xn, wc, wsf, ws, again)
     assert torch.isnan(again[2]).all() and torch.equal(again[[0, 1, 3]], y[[0, 1, 3]])
+
+
+def test_matvec_threads():
+    """Calls from several threads at once, whose kernels want different amounts of shared memory."""
+    shapes = [(m, n, k) for m in (1, 16, 24) for n, k in ((64, 128), (300, 8192), (64, 2048), (8200, 2064))]
+
+    def work(i, out):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for m, n, k in shapes[i:] + shapes[:i]:
+                y, ref, tol = matvec_case(m, n, k, "16", seed=i)
+                out.append(bool(((y.double() - ref).abs() <= tol).all()))
+    outs = [[] for _ in range(4)]
+    threads = [threading.Thread(target=work, args=(3 * i, o)) for i, o in enumerate(outs)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert all(len(o) == len(shapes) and all(o) for o in outs)
 
 
 @pytest.mark.parametrize("dt,k", [("bf16", 144), ("f16", 512), ("f16", 4096)])
