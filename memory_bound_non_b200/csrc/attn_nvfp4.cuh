@@ -3,7 +3,8 @@
 #pragma once
 
 #include "frt_device.cuh"
-#include "frt_host.h"
+#include "frt_fragments.cuh"
+#include "frt_launch.h"
 #include "frt_tensor.cuh"
 
 namespace frt {

@@ -479,7 +479,7 @@ struct ChainArgs {
 
 template <int DT, int K, int QM, int GP, int ACT>
 frt_status launch_chain(const ChainArgs& a, size_t smem, cudaStream_t st) {
-  static SmemOptIn opted;
+  static std::atomic<int> opted{0};
   auto kern = chain_persistent_kernel<DT, K, QM, GP, ACT>;
   const frt_status os = opt_in_smem(kern, smem, opted);
   if (os != FRT_OK) return os;

@@ -4,8 +4,6 @@
 #include <cstdint>
 
 #include <atomic>
-#include <thread>
-
 #include <cuda_runtime.h>
 
 #include <cuda_runtime_api.h>
@@ -54,13 +52,6 @@ inline frt_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t
   return launch_status();
 }
 
-constexpr int kSMs = 148;
-// Clusters of `ranks` CTAs (1, 2, 4 or 8) that the GPU holds at once, per_sm (1, 2
-// or 4) to an SM.  A cluster lies inside one GPC and the GPCs' SMs are no
-// multiple of 4 or 8: 33 of 4 and 15 of 8 where 148 SMs would hold 37 and 18.  A
-// grid cut for the latter runs a second wave, twice the time.
-int cluster_room(int per_sm, int ranks);
-
 // As launch(), with the grid grouped into thread-block clusters of
 // `cluster_x` CTAs along x (co-scheduled; they share distributed shared memory).
 template <typename... KArgs, typename... Args>
@@ -99,36 +90,20 @@ inline bool quant_args_ok(frt_quant qm, const float* static_scale, const float* 
   return block_scales != nullptr && aligned(block_scales, 4);
 }
 
-// Raises a kernel's dynamic shared memory limit on the current device to `bytes`
-// (needed above the 48 KB default); `opted` keeps the largest size that each
-// device has seen.  The limit is set under a lock, so that a thread with a
-// smaller size never lowers it behind one with a larger.
-struct SmemOptIn {
-  static constexpr int kDevices = 64;
-  std::atomic<int> bytes[kDevices] = {};
-  std::atomic_flag busy = ATOMIC_FLAG_INIT;
-};
+// Raises a kernel's dynamic shared memory limit to `bytes` once (the largest
+// size seen so far is kept in `opted`); needed above the 48 KB default.
 template <typename Kern>
-frt_status opt_in_smem(Kern kern, size_t bytes, SmemOptIn& opted) {
-  int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess || device >= SmemOptIn::kDevices) {
-    (void)cudaGetLastError();
-    return FRT_ERR_CUDA;
-  }
-  std::atomic<int>& seen = opted.bytes[device];
-  if ((int)bytes <= seen.load(std::memory_order_acquire)) return FRT_OK;
-  while (opted.busy.test_and_set(std::memory_order_acquire)) std::this_thread::yield();
-  frt_status st = FRT_OK;
-  if ((int)bytes > seen.load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess) {
-      seen.store((int)bytes, std::memory_order_release);
-    } else {
+frt_status opt_in_smem(Kern kern, size_t bytes, std::atomic<int>& opted) {
+  if ((int)bytes > opted.load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
       (void)cudaGetLastError();
-      st = FRT_ERR_CUDA;
+      return FRT_ERR_CUDA;
+    }
+    int cur = opted.load(std::memory_order_relaxed);
+    while ((int)bytes > cur && !opted.compare_exchange_weak(cur, (int)bytes)) {
     }
   }
-  opted.busy.clear(std::memory_order_release);
-  return st;
+  return FRT_OK;
 }
 
 // Validation shared by the NVFP4 producers: scale-factor layout, the global

@@ -236,7 +236,7 @@ struct Args {
 
 template <int DT, int K, bool G, bool MOD, int QM>
 frt_status launch_k(const Args& a, cudaStream_t st) {
-  static SmemOptIn opted;
+  static std::atomic<int> opted{0};
   auto kern = gate_residual_adarms_fp8_kernel<DT, K, G, MOD, QM>;
   const size_t smem = (size_t)((G && K >= 8 ? 1 : 0) + (MOD ? 2 : 0)) * a.C * sizeof(uint4);
   const frt_status os = opt_in_smem(kern, smem, opted);

@@ -23,6 +23,7 @@
 // TwoSum, rstd as a pair from an fp64 sum: 16 fp32 operations an element on K
 // alone (a sixth of the heads of a 32/8 layer).
 #include "frt_device.cuh"
+#include "frt_fragments.cuh"
 #include "frt_host.h"
 
 namespace frt {

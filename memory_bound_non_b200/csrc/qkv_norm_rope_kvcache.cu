@@ -918,7 +918,7 @@ frt_status launch_gp(const Args& a, bool tma, cudaStream_t st) {
   const uint16_t* kw = static_cast<const uint16_t*>(a.kw);
   uint16_t* qo = static_cast<uint16_t*>(a.q_out);
   if (tma) {
-    static SmemOptIn opted;
+    static std::atomic<int> opted{0};
     auto kt = qkv_norm_rope_kvcache_tma_kernel<DT, P, GP, EPI>;
     const size_t smem = tma_smem(a.H, a.Hkv, a.hd, KV8);
     const frt_status os = opt_in_smem(kt, smem, opted);
@@ -971,7 +971,7 @@ frt_status launch_dt(int P, int GP, int epi, const Args& a, bool tma, cudaStream
 // The bulk-copy kernel at its LayerNorm level (EPI 3), P = 8 rows.
 template <int DT, int GP>
 frt_status launch_ln_gp(const Args& a, cudaStream_t st) {
-  static SmemOptIn opted;
+  static std::atomic<int> opted{0};
   auto kt = qkv_norm_rope_kvcache_tma_kernel<DT, 8, GP, 3>;
   const size_t smem = tma_smem(a.H, a.Hkv, a.hd, false);
   const frt_status os = opt_in_smem(kt, smem, opted);
