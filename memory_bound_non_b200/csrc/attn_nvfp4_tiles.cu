@@ -330,8 +330,9 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
     uint32_t p[KT / 4];
 #pragma unroll
     for (int i = 0; i < KT / 4; ++i) {
-      p[i] = Pack16<FRT_F16>::from_float2(ex2_approx(fmaf(__uint_as_float(s[2 * i]), c, shift)),
-                                          ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), c, shift)));
+      const float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                  make_float2(c, c), make_float2(shift, shift));
+      p[i] = Pack16<FRT_F16>::from_float2(ex2_approx(e.x), ex2_approx(e.y));
       sum = add_halves(sum, p[i]);
     }
     if constexpr (KT == 128)
