@@ -13,11 +13,13 @@
 //   p = 2^(s - m + 11) in registers, two threads a row
 //   P -> TMEM (binary16, over S), O += P V  (tcgen05, P from TMEM, O in TMEM)
 // Two CTAs share an SM (hd <= 192), so that one's products run beside the
-// other's conversions and exponentials; that is all the pipelining there is.
-// Measured, 512 tokens of 16/8 heads of 128 over 4608 positions: 47.5 us, 390
-// TFLOP/s (the warps' products took 142 us); a tile takes 3700 clocks of an SM
-// against the 1024 of its bound, in barriers and in the latency of what stands
-// between them; a call costs 10 us before and behind its tiles.
+// other's conversions and exponentials.  Inside a CTA only the warp that issues P V
+// waits for all of P and V; the others go on to the next tile's K.
+// Measured, 512 tokens of 16/8 heads of 128 over 4608 positions: 46.3 us, 394
+// TFLOP/s (the warps' products took 142 us; with block-wide barriers in those
+// places and one exponential's argument to an instruction 47.9); a tile takes
+// 3600 clocks of an SM against the 1024 of its bound, in the latency of its
+// dependent steps; a call costs 10 us before and behind its tiles.
 //
 // Operand layouts: Q and K as rows of 64 dimensions (128 bytes) with the
 // 128-byte swizzle, k-major; V in the same form, which read as the B operand of
@@ -76,7 +78,8 @@ struct Small {  // behind the operands
   uint32_t nan[4];            // keys of the tile with a NaN factor in V
   float2 ml[kTileRows];       // (maximum, sum) of a row, for the cluster
   float factor[8][kTileRows];
-  uint64_t s_done, o_done, drained;
+  uint64_t s_done, o_done, drained;  // products
+  uint64_t v_ready, p_ready;         // a tile's V and P, an arrival of each warp
   uint32_t tmem;
   int gave_up;
 };
@@ -116,6 +119,8 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
     mbar_init(&sm.s_done, 1);
     mbar_init(&sm.o_done, 1);
     mbar_init(&sm.drained, 1);
+    mbar_init(&sm.v_ready, kThreads / 32);
+    mbar_init(&sm.p_ready, kThreads / 32);
     mbar_init_fence();
     sm.gave_up = 0;
   }
@@ -267,6 +272,8 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
     __syncwarp();
     convert(v_raw, v_smem, true);
     fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.v_ready);
     load(a.k_codes, a.k_sf, tile + 1, k_raw);
 
     wait(&sm.s_done, nth & 1);
@@ -292,9 +299,10 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
     for (int i = 1; i < KT / 2; ++i) top = fmaxf(top, __uint_as_float(s[i]));
     sm.top[half][row] = top;
     tc_fence_before();
-    __syncthreads();
+    pair_sync(1 + (warp & 3));  // the other half's maxima are there, and its part of S is read (P lies over S)
     const float c = sm.scale[row];
     top = fmaxf(top, sm.top[half ^ 1][row]) * c;
+    wait(&sm.v_ready, nth & 1);
     // a NaN factor in V: the weight of its key turns NaN for the rows that see it
 #pragma unroll
     for (int w = 0; w < KT / 64; ++w) {
@@ -341,16 +349,21 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
       tc_st16(s_tmem + half * 16, p);
     tc_wait_st();
     tc_fence_before();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < KT / 16; ++k)
-        tc_mma_tmem(tmem + T::kO, tmem + 8 * k, smem_operand(v_smem + k * 2048, kRegion, 1024),
-                    product_desc(HD, true), nth > 0 || k > 0);
-      tc_commit(&sm.o_done);
-    }
     __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.p_ready);
+    if (warp == 0) {  // (the others go on to the next tile's K)
+      wait(&sm.p_ready, nth & 1);
+      __syncwarp();
+      if (lane == 0) {
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k)
+          tc_mma_tmem(tmem + T::kO, tmem + 8 * k, smem_operand(v_smem + k * 2048, kRegion, 1024),
+                      product_desc(HD, true), nth > 0 || k > 0);
+        tc_commit(&sm.o_done);
+      }
+      __syncwarp();
+    }
   }
 
   // ---- output

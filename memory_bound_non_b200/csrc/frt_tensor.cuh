@@ -97,6 +97,11 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// A barrier of two warps; id 1 .. 15.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 // ------------------------------------------------------------- clusters --
 // Cluster-wide barrier, and loads from the shared memory of its CTA `rank`.
 __device__ __forceinline__ void cluster_sync() {
