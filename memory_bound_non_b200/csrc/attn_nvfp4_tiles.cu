@@ -49,7 +49,8 @@ struct Tile {
   static constexpr int kO = KT;                             // first column of O
   // (a cluster's parts, 128 rows of HD floats, fit over the operands)
   static_assert(kTileRows * HD * 4 <= C * (kQRegion + 2 * kRegion), "parts over the operands");
-  static constexpr size_t kSmem = 1024 + C * (kQRegion + 2 * kRegion) + kSmallBytes;
+  static constexpr size_t kUsed = 1024 + C * (kQRegion + 2 * kRegion) + kSmallBytes;
+  static constexpr size_t kSmem = kUsed > tmem_smem(kCols) ? kUsed : tmem_smem(kCols);
 };
 
 // x plus both halves of w, one rounding each.
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
   const Place place = place_of(a);
   const int kvh = place.kvh, rt = place.rt, chunk = place.chunk;
 
-  pdl_enter();
+  pdl_wait();
   const Seq seq = sequence(a, b);
   const RowRange range = row_range<kTileRows>(a, seq, rt * kTileRows, kvh);
   if (range.bad && a.status != nullptr) atomicOr(a.status, 1);
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, HD > 192 ? 1 : 2) tiles_kernel(const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_release();
   const uint32_t tmem = sm.tmem;
   const uint32_t s_tmem = tmem + ((uint32_t)(warp & 3) << 21), o_tmem = s_tmem + T::kO;
 

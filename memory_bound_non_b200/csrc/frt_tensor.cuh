@@ -12,6 +12,20 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Tensor memory is never waited for.  tc_alloc blocks while the SM's 512 columns
+// are taken, without a bound, so nothing that holds columns may depend on what is
+// blocked:
+//   * a kernel allocates behind pdl_wait and calls pdl_release behind its
+//     allocation (every thread, after the block's barrier), so columns are never
+//     held across the wait for a grid that has yet to allocate;
+//   * a kernel asks for tmem_smem(COLS) bytes of shared memory at least, its share
+//     of an SM's by columns, so that CTAs (of any streams, and of clusters, which
+//     wait for one another) whose columns do not fit together never share an SM.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+constexpr size_t tmem_smem(int cols) { return (size_t)cols * 448; }
+static_assert((512 + 32) * 448 + 1024 > 228 * 1024 && tmem_smem(512) <= 227 * 1024,
+              "544 columns exceed an SM's shared memory (with the 1 KB that a CTA takes besides), 512 fit a CTA");
 template <int COLS>
 __device__ __forceinline__ void tc_alloc(uint32_t* where) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)), "n"(COLS)

@@ -36,6 +36,7 @@ template <int NX>
 struct Tile {
   static constexpr int kA = 2 * kRegionA, kB = 2 * NX * 128, kStage = kA + kB;
   static constexpr size_t kSmem = 1024 + 2 * kStage + 3 * NX * 4 + 64;
+  static_assert(kSmem >= tmem_smem(2 * NX), "tensor memory is never waited for");
 };
 
 struct RawX {
@@ -172,16 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
     mbar_init_fence();
     *gave_up_at = 0;
   }
-  if (warp == 0) {
-    __syncwarp();
-    tc_alloc<kCols>(tmem_at);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_at;
-  const uint32_t my_tmem = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * kQ;
-  pdl_enter();
+  pdl_wait();
 
   // x: half-warp h takes rows h, h + 32, ..
   const int h = threadIdx.x >> 4, l = threadIdx.x & 15;
@@ -193,6 +185,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
     x_row[i].set(a, h + 32 * i, g0, l);
     x[i] = x_row[i].next(a, h + 32 * i < a.rows && k_left > 0);
   }
+  if (warp == 0) {
+    __syncwarp();
+    tc_alloc<kCols>(tmem_at);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  const uint32_t my_tmem = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * kQ;
+  pdl_release();
 
   bool gave_up = false;
   auto wait = [&](int b, int phase) {

@@ -1,6 +1,8 @@
 """Host-side refusals of the NVFP4 operators: the C entry points reject bad
 arguments before any CUDA call (fake, never-dereferenced pointers), and the
 binding rejects tensors that do not fit."""
+import os
+
 import pytest
 import torch
 
@@ -113,3 +115,22 @@ def test_binding_rejects_host_tensors():
 def test_kv_sf_shape():
     assert frt.nvfp4_kv_sf_shape(1, 2, 64) == (1, 2, 4, 4)
     assert frt.nvfp4_kv_sf_shape(9, 1, 256) == (3, 1, 16, 4)
+
+
+def _kernel_text(source):
+    """The text of the one kernel of a source file that uses tensor memory."""
+    root = os.path.join(os.path.dirname(frt.__file__), "csrc", source)
+    with open(root) as f:
+        text = f.read()
+    return text[text.index("tiles_kernel("):text.index("tc_free<")]
+
+
+@pytest.mark.parametrize("source", ["attn_nvfp4_tiles.cu", "matvec_nvfp4_tiles.cu"])
+def test_tensor_memory_is_never_held_across_a_dependency(source):
+    """An allocation of tensor memory blocks without a bound while an SM's columns are taken.  A kernel that held
+    columns while it waits for the grid before it, or let the next grid in before it has its own, could block that
+    grid for good: the order in the source is wait, allocate, release."""
+    body = _kernel_text(source)
+    assert "pdl_enter" not in body  # waits and releases at once
+    assert body.index("pdl_wait();") < body.index("tc_alloc<") < body.index("pdl_release();")
+    assert body.index("tc_alloc<") < body.index("__syncthreads();", body.index("tc_alloc<")) < body.index("pdl_release();")

@@ -847,3 +847,29 @@ def test_in_bounds():
                                         (20, 8210, 2064, "e4m3", "rows"), (32, 4100, 4128, "16", "swizzled"))]
     for fn in (attn, cache, matvec):
         both_builds(fn)
+
+
+@pytest.mark.parametrize("hd", [64, 192, 256])
+def test_attention_then_output_product(hd):
+    """The two kernels that allocate tensor memory, one behind the other on a stream and on two streams at once:
+    attention over many rows and the product of its output."""
+    cases = [Case([200], [900], 8, 1, hd, seed=s) for s in (1, 2)]
+    g = gen(hd)
+    wc, wsf, ws, w = weights(512, 8 * hd, g, "rows")
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[(torch.empty_like(c.q), torch.empty((200, 512), dtype=c.q.dtype, device=DEV)) for _ in range(4)] for c in cases]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for c, st, o in zip(cases, streams, outs):
+            att, y = o[i]
+            frt.frt_attn_nvfp4_kvcache(c.q, *c.cache.args, c.kv_len, att, c.scale, max_kv_len=900, stream=st)
+            frt.frt_matvec_nvfp4(att.view(200, 8 * hd), wc, wsf, ws, y, stream=st)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        ref, tol = c.expected()
+        x = o[0][0].view(200, -1).double()
+        assert ((o[0][0].double() - ref).abs() <= tol).all()
+        y = x @ w.t()
+        assert ((o[0][1].double() - y).abs() <= P.matvec_bound(x, w, y, c.q.dtype)).all()
+        for att, again in o[1:]:
+            assert torch.equal(att, o[0][0]) and torch.equal(again, o[0][1])
