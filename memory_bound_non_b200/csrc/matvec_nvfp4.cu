@@ -64,8 +64,9 @@ struct WRows {
                                                               : (int64_t)row * (a.K >> 4));
     }
   }
-  __device__ __forceinline__ int sf_at(const Args& a, int col) const {
-    return LAY == 2 || (LAY == 0 && a.swizzled) ? (col >> 2) * 512 + (col & 3) : col;
+  // (swizzled: 128 bytes a column, past 32 bits from K = 2^28 on)
+  __device__ __forceinline__ int64_t sf_at(const Args& a, int col) const {
+    return LAY == 2 || (LAY == 0 && a.swizzled) ? (int64_t)(col >> 2) * 512 + (col & 3) : col;
   }
   // Group `base` + u; whole: the sets' four groups lie inside K.
   __device__ __forceinline__ void load(const Args& a, int base, int u, bool whole, int t, WFrag& f) const {

@@ -873,3 +873,31 @@ def test_attention_then_output_product(hd):
         assert ((o[0][1].double() - y).abs() <= P.matvec_bound(x, w, y, c.q.dtype)).all()
         for att, again in o[1:]:
             assert torch.equal(att, o[0][0]) and torch.equal(again, o[0][1])
+
+
+@pytest.mark.parametrize("m,k", [(1, 2 ** 28 + 4096), (3, 2 ** 28 + 2064), (12, 2 ** 28 + 288)])
+def test_matvec_swizzled_factors_past_32_bits(m, k):
+    """Swizzled factors of columns behind 2^31 bytes.  x is zero but at some columns of each quarter of K, and the
+    factors of all other blocks are zeros."""
+    g = gen(m)
+    n = 3
+    # whole blocks: the first, the last, and both sides of 2^28
+    cols = torch.unique(torch.cat([torch.arange(b * 16, b * 16 + 16, device=DEV)
+                                   for b in (0, 5, k // 64, k // 32, 2 ** 24 - 1, 2 ** 24, k // 16 - 2, k // 16 - 1)]))
+    x = torch.zeros((m, k), dtype=torch.float16, device=DEV)
+    xv = randn((m, cols.numel()), g).half()
+    x[:, cols] = xv
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, device=DEV, dtype=torch.uint8)
+    atoms = -(-(k // 16) // 4)
+    sf = torch.zeros((atoms * 512,), dtype=torch.uint8, device=DEV)
+    blocks = cols[::16] // 16
+    factors = torch.randint(40, 80, (n, blocks.numel()), generator=g, device=DEV, dtype=torch.uint8)
+    for r in range(n):
+        sf[blocks // 4 * 512 + r * 16 + blocks % 4] = factors[r]
+    scale = torch.tensor([0.01], device=DEV)
+    y = torch.empty((m, n), dtype=torch.float16, device=DEV)
+    frt.frt_matvec_nvfp4(x, codes, sf, scale, y, sf_layout="swizzled")
+    w = P.decode(codes[:, cols[::2] // 2], factors, scale[0])
+    ref = xv.double() @ w.t()
+    # products by zero leave the sums as they are: the bound counts the columns that are not
+    assert ((y.double() - ref).abs() <= P.matvec_bound(xv.double(), w, ref, torch.float16)).all()
