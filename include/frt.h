@@ -539,7 +539,7 @@ typedef enum { FRT_X_16BIT = 0, FRT_X_E4M3 = 1, FRT_X_E4M3_BLOCK = 2, FRT_X_NVFP
 
 /*
  * Matrix-vector products with NVFP4 weights, for the few rows of a decoding or
- * action step (any M is accepted; the weights are read once per 128 rows):
+ * action step (M may be large; the weights are read once per 128 rows):
  *   y[i, n] = sum_k x[i, k] w[n, k] + bias[n],
  *   w[n, k] = e2m1 code * sf[n, k / 16] * w_scale,
  * x as the 16-bit type or as this library's FP8 / NVFP4 ops wrote it.  Products
@@ -563,7 +563,7 @@ typedef enum { FRT_X_16BIT = 0, FRT_X_E4M3 = 1, FRT_X_E4M3_BLOCK = 2, FRT_X_NVFP
  *   x, w_codes, x_sf and w_sf 16-byte aligned; bias and y 2-byte, x_scales and
  *   w_scale 4-byte.
  *   Layout rule: N > 0, K > 0 and K % 16 == 0.  M == 0 does nothing.
- *   Unsupported: N or K > 2^31 - 65536.
+ *   Unsupported: M, N or K > 2^31 - 65536.
  */
 frt_status frt_matvec_nvfp4(const void* x, const float* x_scales, const uint8_t* x_sf, const uint8_t* w_codes,
                             const uint8_t* w_sf, const float* w_scale, const void* bias, void* y, int M, int N, int K,

@@ -549,7 +549,7 @@ constexpr int64_t kManyWeights = 1 << 24;
 bool warps_win(const Args& a) {
   return a.rows <= kFewRows || (a.rows <= kMoreRows && (int64_t)a.N * a.K >= kManyWeights);
 }
-constexpr int kMaxSize = 0x7FFF0000;  // (32-bit indices reach past N and K by less than 65536)
+constexpr int kMaxSize = 0x7FFF0000;  // (32-bit indices reach past M, N and K by less than 65536)
 frt_status launch_rows(Args a, cudaStream_t stream) {
   for (a.m0 = 0; a.m0 < a.M; a.m0 += kTileXRows) {
     a.rows = std::min(a.M - a.m0, kTileXRows);
@@ -574,7 +574,7 @@ extern "C" frt_status frt_matvec_nvfp4(const void* x, const float* x_scales, con
   if (M < 0 || N <= 0 || K <= 0 || K % 16 != 0 || x_format < FRT_X_16BIT || x_format > FRT_X_NVFP4 ||
       (sf_layout != FRT_SF_ROW_MAJOR && sf_layout != FRT_SF_SWIZZLED_128X4) || !valid_dtype(dt))
     return FRT_ERR_INVALID_ARG;
-  if (N > kMaxSize || K > kMaxSize) return FRT_ERR_UNSUPPORTED;
+  if (M > kMaxSize || N > kMaxSize || K > kMaxSize) return FRT_ERR_UNSUPPORTED;
   if (M == 0) return FRT_OK;
   for (const void* p : {x, (const void*)w_codes, (const void*)w_sf})
     if (p == nullptr || !aligned(p, 16)) return FRT_ERR_INVALID_ARG;

@@ -134,3 +134,9 @@ def test_tensor_memory_is_never_held_across_a_dependency(source):
     assert "pdl_enter" not in body  # waits and releases at once
     assert body.index("pdl_wait();") < body.index("tc_alloc<") < body.index("pdl_release();")
     assert body.index("tc_alloc<") < body.index("__syncthreads();", body.index("tc_alloc<")) < body.index("pdl_release();")
+
+
+@pytest.mark.parametrize("m", [2 ** 31 - 65535, 2 ** 31 - 128, 2 ** 31 - 1])
+def test_matvec_refuses_rows_at_the_end_of_32_bits(m):
+    """The rows are taken 128 at a time by a 32-bit index, which must not run past its end."""
+    assert matvec_call(M=m) == UNSUP
