@@ -505,6 +505,11 @@ frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8_t* k_sf, c
  *                 contents need no preparation and mean nothing afterwards).
  *                 Calls that may run at the same time need one each.  NULL if
  *                 that size is 0.
+ *                 The size never falls with a larger M or max_kv_len (the other
+ *                 arguments alike), and a call takes any workspace that it fits:
+ *                 one of a program's largest M and max_kv_len serves all its
+ *                 calls of that n_seqs and max_q_len.  (A larger n_seqs or
+ *                 max_q_len may want less: fewer chunks fill the GPU.)
  *   status        device int32[1] or NULL; bits set with an atomic OR, never
  *                 cleared:  bit 0  a kv_len below 0 or above max_kv_len, or one
  *                 that reaches past the capacity or the page table (clamped);

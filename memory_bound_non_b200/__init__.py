@@ -392,8 +392,9 @@ def frt_nvfp4_kvcache_read(k_codes, k_sf, v_codes, v_sf, kv_scales, slots, k_out
 
 def attn_nvfp4_workspace(q, Hkv, max_kv_len, n_seqs=1, max_q_len=None):
     """A workspace tensor for frt_attn_nvfp4_kvcache calls of these sizes, on
-    q's device (None where the call needs none).  Calls that may run at the
-    same time need one each."""
+    q's device (None where they need none).  It serves calls with fewer tokens
+    and a smaller max_kv_len too, n_seqs and max_q_len alike.  Calls that may
+    run at the same time need one each."""
     M, Hq, hd = q.shape
     n = load().frt_attn_nvfp4_workspace_bytes(M, n_seqs, Hq, Hkv, hd, max(M, 1) if max_q_len is None else max_q_len,
                                               max_kv_len)

@@ -736,51 +736,82 @@ struct Plan {
   int nt;  // 0: the tile kernel
   int row_tiles, chunks, chunk_tiles, cluster, keys;
 };
+// What the sizes but max_kv_len say of a kernel (nt as in Plan).
+struct Cut {
+  int keys;              // positions of a tile
+  int64_t row_tiles, ctas;
+  int64_t least;         // a CTA's smallest share: a tile for every warp
+  int per_sm;            // CTAs
+  int64_t at_once;       // on the GPU
+  int64_t in_cluster;    // CTAs that a cluster may have without a second wave
+  int64_t most;          // chunks of a row tile, where there are more
+};
+Cut cut_of(int nt, int64_t rows, int n_seqs, int Hkv, int hd) {
+  Cut c;
+  const int build = hd <= 64 ? 64 : hd <= 128 ? 128 : hd <= 192 ? 192 : 256;
+  const int tile_rows = nt == 0 ? kTileRows : 8 * nt;
+  c.keys = nt == 0 ? tile_keys(hd) : kTile;
+  c.row_tiles = (rows + tile_rows - 1) / tile_rows;
+  // (below 2^63 for sizes that the call takes; more than a grid holds is as good as that)
+  c.ctas = std::min(c.row_tiles * Hkv * n_seqs, (int64_t)1 << 40);
+  c.least = nt == 0 ? 1 : attn_warps(build, nt);
+  c.per_sm = nt == 0 ? (hd > 192 ? 1 : 2) : 16 / attn_warps(build, nt);
+  c.at_once = (int64_t)kSMs * c.per_sm;
+  c.in_cluster = 1;
+  while (c.in_cluster < 8 && c.ctas * c.in_cluster * 2 <= c.at_once) c.in_cluster *= 2;
+  // sequences whose lengths differ get twice as many CTAs as run at once
+  c.most = c.at_once * (n_seqs > 1 ? 2 : 1) / c.ctas;
+  return c;
+}
+int64_t tiles_in(const Cut& c, int64_t max_kv_len) { return max_kv_len > 0 ? (max_kv_len + c.keys - 1) / c.keys : 1; }
+// More chunks than a cluster has CTAs cost a second kernel and a way through
+// memory, about as long as kJoinRounds tiles of a warp (or CTA) take.  (By sizes
+// alone: the caller asks for the workspace before the call, and perhaps without a
+// GPU.)
+constexpr int64_t kJoinRounds = 8;
+// Tiles of a chunk where a second kernel joins them, else 0.
+int64_t joined_tiles(const Cut& c, int64_t tiles) {
+  if (c.in_cluster == 1) return 0;
+  int64_t per = (tiles + c.most - 1) / c.most;
+  per = (per + c.least - 1) / c.least * c.least;
+  return tiles / (c.in_cluster * c.least) > per / c.least + kJoinRounds ? per : 0;
+}
+// The most chunks that any call of up to so many tiles is joined from.  (A chunk
+// has `least` tiles or more, whole multiples of them, so the count itself falls
+// and rises with the length.)
+int64_t joined_chunks(const Cut& c, int64_t tiles) {
+  if (c.in_cluster == 1 || tiles / (c.in_cluster * c.least) <= 1 + kJoinRounds) return 0;
+  return std::min(c.most, (tiles + c.least - 1) / c.least);
+}
 // The tile kernel takes calls with at least kManyRows rows to a sequence and KV
 // head and kManyPairs (row, key) pairs times hd / 128: a call of it costs about
 // 10 us and does 1 M such pairs in a microsecond, the kernel for few rows 5 us
 // and 0.27 M.
 constexpr int64_t kManyRows = 48, kManyPairs = 2500000;
-// for_workspace: whether and how a second kernel joins the chunks, no more.
-Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len, bool for_workspace) {
+double pairs_a_key(int64_t rows, int n_seqs, int Hkv, int hd) { return (double)rows * Hkv * n_seqs * hd / 128; }
+int few_rows_nt(int64_t rows, int n_seqs, int Hkv, int hd) {
+  // 32 rows to a CTA only where 16 would fill the GPU already
+  const bool small = (double)((rows + 15) / 16) * Hkv * n_seqs * 8 < kSMs * 3;
+  return rows <= 8 ? 1 : rows <= 16 || hd > 128 || small ? 2 : 4;
+}
+Plan make_plan(int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
   Plan p;
   const int64_t rows = (int64_t)max_q_len * (Hq / Hkv);
-  const double pairs = (double)rows * Hkv * n_seqs * max_kv_len * hd / 128;
-  // 32 rows to a CTA only where 16 would fill the GPU already
-  const bool small = (rows + 15) / 16 * Hkv * n_seqs * 8 < kSMs * 3;
-  p.nt = rows >= kManyRows && pairs >= kManyPairs ? 0 : rows <= 8 ? 1 : rows <= 16 || hd > 128 || small ? 2 : 4;
-  const int tile_rows = p.nt == 0 ? kTileRows : 8 * p.nt;
-  p.keys = p.nt == 0 ? tile_keys(hd) : kTile;
-  const int64_t row_tiles = (rows + tile_rows - 1) / tile_rows;
-  p.row_tiles = (int)(row_tiles > 0x7FFFFFFF ? 0x7FFFFFFF : row_tiles);
-  const int64_t tiles = max_kv_len > 0 ? ((int64_t)max_kv_len + p.keys - 1) / p.keys : 1;
-  const int64_t ctas = row_tiles * Hkv * n_seqs;
-  // a CTA's smallest share: a tile for every warp
-  const int build = hd <= 64 ? 64 : hd <= 128 ? 128 : hd <= 192 ? 192 : 256;
-  const int64_t least = p.nt == 0 ? 1 : attn_warps(build, p.nt);  // tiles
-  const int per_sm = p.nt == 0 ? (hd > 192 ? 1 : 2) : 16 / attn_warps(build, p.nt);
+  const bool many = rows >= kManyRows && pairs_a_key(rows, n_seqs, Hkv, hd) * max_kv_len >= kManyPairs;
+  p.nt = many ? 0 : few_rows_nt(rows, n_seqs, Hkv, hd);
+  const Cut cut = cut_of(p.nt, rows, n_seqs, Hkv, hd);
+  const int64_t tiles = tiles_in(cut, max_kv_len), ctas = cut.ctas, least = cut.least;
+  const int per_sm = cut.per_sm;
+  p.keys = cut.keys;
+  p.row_tiles = (int)(cut.row_tiles > 0x7FFFFFFF ? 0x7FFFFFFF : cut.row_tiles);
   p.cluster = 0;
   p.chunks = 1;
   p.chunk_tiles = (int)tiles;
-  // More chunks than a cluster has CTAs cost a second kernel and a way through
-  // memory, about as long as kJoinRounds tiles of a warp (or CTA) take.  Sequences
-  // whose lengths differ get twice as many CTAs as run at once.  (By sizes alone:
-  // the caller asks for the workspace before the call, and perhaps without a GPU.)
-  constexpr int64_t kJoinRounds = 8;
-  const int64_t at_once = (int64_t)kSMs * per_sm;
-  int64_t in_cluster = 1;
-  while (in_cluster < 8 && ctas * in_cluster * 2 <= at_once) in_cluster *= 2;
-  if (in_cluster > 1) {
-    const int64_t most = at_once * (n_seqs > 1 ? 2 : 1) / ctas;
-    int64_t per = (tiles + most - 1) / most;
-    per = (per + least - 1) / least * least;
-    if (tiles / (in_cluster * least) > per / least + kJoinRounds) {
-      p.chunk_tiles = (int)per;
-      p.chunks = (int)((tiles + per - 1) / per);
-      return p;
-    }
+  if (const int64_t per = joined_tiles(cut, tiles)) {
+    p.chunk_tiles = (int)per;
+    p.chunks = (int)((tiles + per - 1) / per);
+    return p;
   }
-  if (for_workspace) return p;
   // The keys among the CTAs of a cluster: the cheapest of 1, 2, 4 and 8, in turns
   // of a CTA (a tile for each warp) on a full SM.  A CTA costs about 2.5 besides
   // its turns (measured: 5.5 to 7 us beside turns of 2.4 at hd 128, 4.3 beside 1.6
@@ -809,9 +840,15 @@ void divisor(int d, uint32_t* mul, int* shift) {
   *mul = (uint32_t)((((1ULL << *shift) - d) << 32) / d + 1);
 }
 
-bool plan_args_ok(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
-  return M >= 0 && n_seqs > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && hd > 0 && hd % 16 == 0 && max_q_len > 0 &&
-         max_kv_len >= 0;
+frt_status check_sizes(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len, int max_kv_len) {
+  if (M < 0 || n_seqs <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || hd <= 0 || hd % 16 != 0 || max_q_len <= 0 ||
+      max_kv_len < 0)
+    return FRT_ERR_INVALID_ARG;
+  return hd > 256 || Hq > 1 << 20 || n_seqs > 65535 || max_kv_len > 0x7FFFFF00 ? FRT_ERR_UNSUPPORTED : FRT_OK;
+}
+
+size_t workspace_bytes_of(int M, int Hq, int hd, int64_t chunks) {
+  return (size_t)M * Hq * (chunks * (8 + 4 * (size_t)hd) + 4);
 }
 
 template <int HD, bool EXACT, int NT>
@@ -845,10 +882,20 @@ using namespace frt;
 
 extern "C" size_t frt_attn_nvfp4_workspace_bytes(int M, int n_seqs, int Hq, int Hkv, int hd, int max_q_len,
                                                  int max_kv_len) {
-  if (!plan_args_ok(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len)) return 0;
-  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len, true);
-  if (p.chunks == 1) return 0;
-  return (size_t)M * Hq * (p.chunks * (8 + 4 * (size_t)hd) + 4);
+  if (check_sizes(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len) != FRT_OK) return 0;
+  // what the longest call that the kernel for few rows takes may want, and, if
+  // some are the tile kernel's, the longest of all
+  const int64_t rows = (int64_t)max_q_len * (Hq / Hkv);
+  const double pairs = pairs_a_key(rows, n_seqs, Hkv, hd);
+  int64_t few_len = max_kv_len, chunks = 0;
+  if (rows >= kManyRows && pairs * max_kv_len >= kManyPairs) {
+    few_len = std::min(few_len, (int64_t)(kManyPairs / pairs) + 1);
+    const Cut cut = cut_of(0, rows, n_seqs, Hkv, hd);
+    chunks = joined_chunks(cut, tiles_in(cut, max_kv_len));
+  }
+  const Cut cut = cut_of(few_rows_nt(rows, n_seqs, Hkv, hd), rows, n_seqs, Hkv, hd);
+  chunks = std::max(chunks, joined_chunks(cut, tiles_in(cut, few_len)));
+  return chunks == 0 ? 0 : workspace_bytes_of(M, Hq, hd, chunks);
 }
 
 extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_codes, const uint8_t* k_sf,
@@ -859,12 +906,12 @@ extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_cod
                                              int Hkv, int hd, int capacity, int page_size, int max_pages,
                                              int max_q_len, int max_kv_len, int window, float softmax_scale,
                                              frt_dtype dt, cudaStream_t stream) {
-  if (!plan_args_ok(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len) || capacity <= 0 || !std::isfinite(softmax_scale) ||
-      !valid_dtype(dt))
+  const frt_status sizes = check_sizes(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
+  if (sizes == FRT_ERR_INVALID_ARG || capacity <= 0 || !std::isfinite(softmax_scale) || !valid_dtype(dt))
     return FRT_ERR_INVALID_ARG;
   if (page_table != nullptr && (page_size <= 0 || page_size % 4 != 0 || max_pages < 0)) return FRT_ERR_INVALID_ARG;
   if (q_indptr == nullptr && n_seqs != 1) return FRT_ERR_INVALID_ARG;
-  if (hd > 256 || Hq > 1 << 20 || n_seqs > 65535 || max_kv_len > 0x7FFFFF00) return FRT_ERR_UNSUPPORTED;
+  if (sizes != FRT_OK) return sizes;
   if (M == 0) return FRT_OK;
   for (const void* p : {q, (const void*)k_codes, (const void*)k_sf, (const void*)v_codes, (const void*)v_sf,
                         (const void*)out})
@@ -872,10 +919,11 @@ extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_cod
   if (kv_scales == nullptr || !aligned(kv_scales, 4) || kv_len == nullptr || !aligned(kv_len, 4) ||
       !aligned(q_indptr, 4) || !aligned(page_table, 4) || !aligned(status, 4))
     return FRT_ERR_INVALID_ARG;
-  const size_t need = frt_attn_nvfp4_workspace_bytes(M, n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
-  if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
+  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len);
+  const bool joined = p.chunks > 1 && !p.cluster;  // by a second kernel
+  if (joined && (workspace == nullptr || !aligned(workspace, 16) ||
+                 workspace_bytes < workspace_bytes_of(M, Hq, hd, p.chunks)))
     return FRT_ERR_INVALID_ARG;
-  const Plan p = make_plan(n_seqs, Hq, Hkv, hd, max_q_len, max_kv_len, false);
   Args a = {};
   a.q = q;
   a.k_codes = k_codes;
@@ -922,7 +970,7 @@ extern "C" frt_status frt_attn_nvfp4_kvcache(const void* q, const uint8_t* k_cod
                         : p.nt == 1 ? launch_hd<1>(a, stream)
                         : p.nt == 2 ? launch_hd<2>(a, stream)
                                     : launch_hd<4>(a, stream);
-  if (st != FRT_OK || a.chunks == 1 || a.cluster) return st;
+  if (st != FRT_OK || !joined) return st;
   // rows of a sequence and KV head: no more than max_q_len tokens'
   const int64_t warps = (int64_t)max_q_len * a.group * Hkv;
   const bool many = p.chunks > 8;

@@ -140,3 +140,18 @@ def test_tensor_memory_is_never_held_across_a_dependency(source):
 def test_matvec_refuses_rows_at_the_end_of_32_bits(m):
     """The rows are taken 128 at a time by a 32-bit index, which must not run past its end."""
     assert matvec_call(M=m) == UNSUP
+
+
+@pytest.mark.parametrize("hq,hkv,hd,n_seqs,q", [(8, 2, 128, 1, 1), (8, 2, 128, 3, 1), (32, 8, 128, 1, 1), (8, 1, 64, 1, 1),
+                                                (8, 8, 256, 1, 1), (40, 2, 128, 1, 1), (8, 1, 256, 1, 10), (8, 1, 256, 1, 41),
+                                                (16, 8, 128, 1, 41), (4, 2, 80, 2, 5), (16, 1, 64, 1, 300), (8, 2, 192, 1, 17)])
+def test_attn_workspace_never_falls_with_the_length(hq, hkv, hd, n_seqs, q):
+    """A workspace of a program's longest call serves its shorter ones: all tile counts, and more tokens."""
+    W = frt.load().frt_attn_nvfp4_workspace_bytes
+    last = 0
+    for n in list(range(0, 270000, 32)) + [2 ** 20, 2 ** 24, 2 ** 31 - 256]:
+        size = W(q * n_seqs, n_seqs, hq, hkv, hd, q, n)
+        assert size >= last, n
+        last = size
+        if n % 4096 == 0:
+            assert W(1, n_seqs, hq, hkv, hd, q, n) <= size <= W(2 * q * n_seqs, n_seqs, hq, hkv, hd, q, n)

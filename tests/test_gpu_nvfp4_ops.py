@@ -901,3 +901,15 @@ def test_matvec_swizzled_factors_past_32_bits(m, k):
     ref = xv.double() @ w.t()
     # products by zero leave the sums as they are: the bound counts the columns that are not
     assert ((y.double() - ref).abs() <= P.matvec_bound(xv.double(), w, ref, torch.float16)).all()
+
+
+@pytest.mark.parametrize("hq,hkv,hd,q,longest", [(8, 2, 128, 1, 200000), (8, 1, 64, 1, 120000), (8, 1, 256, 41, 30000)])
+def test_attn_one_workspace_for_all_lengths(hq, hkv, hd, q, longest):
+    """The workspace of the longest call serves every shorter one, whose parts may be more: refused by none, and the
+    same bits as with one of its own."""
+    c = Case([q], [longest], hq, hkv, hd)
+    ws = frt.attn_nvfp4_workspace(c.q, hkv, longest, max_q_len=q)
+    for n in (longest, longest - 10584, longest * 9 // 10, longest // 2 + 1, longest // 3, longest // 10, 100):
+        c.kv_len = torch.arange(n - q + 1, n + 1, dtype=torch.int32, device=DEV)
+        ws.fill_(0xFF)
+        assert torch.equal(c.run(workspace=ws, max_kv_len=n), c.run(max_kv_len=n)), n
