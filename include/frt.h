@@ -430,7 +430,9 @@ frt_status frt_gate_residual_adarms_fp8(const void* x, const void* gate, const v
  * q_out as frt_qkv_norm_rope_kvcache; K after norm and RoPE, and V, are
  * quantised in 16-element blocks:
  *   y      = the exact K (or V) element rounded once to fp32 (K: norm and RoPE
- *            carried in pairs of fp32 numbers, about 2^-45 relative),
+ *            carried in pairs of fp32 numbers, about 2^-45 relative, for x and
+ *            x k_norm_w below 2^100; Q's sum of squares is fp32 as in op (b),
+ *            whose range ends at elements of 2^64),
  *   sf     = e4m3(RN(amax_block * RN(1 / RN(6 gs))))   (RNE, saturating),
  *   code   = e2m1(RN(y * RN(1 / RN(sf * gs))))         (RNE, saturating; 0
  *            where sf is 0),

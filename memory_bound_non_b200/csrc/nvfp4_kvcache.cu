@@ -205,11 +205,15 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(WriteArgs a) {
     Split32 r;
     r.hi = 1.0f;
     if (normed) {
-      double ss = 0.0;  // the squares of 16-bit values are exact in fp32
+      // squared in fp64: bf16 values reach past the square root of fp32's range, both ways
+      double ss = 0.0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        ss += ((double)(lo[e].x * lo[e].x) + (double)(lo[e].y * lo[e].y)) +
-              ((double)(hi[e].x * hi[e].x) + (double)(hi[e].y * hi[e].y));
+      for (int e = 0; e < 4; ++e) {
+        ss = fma((double)lo[e].x, (double)lo[e].x, ss);
+        ss = fma((double)lo[e].y, (double)lo[e].y, ss);
+        ss = fma((double)hi[e].x, (double)hi[e].x, ss);
+        ss = fma((double)hi[e].y, (double)hi[e].y, ss);
+      }
       if (lane % P >= a.L) ss = 0.0;  // (a copy of another lane)
 #pragma unroll
       for (int o = P / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);

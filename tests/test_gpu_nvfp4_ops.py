@@ -913,3 +913,21 @@ def test_attn_one_workspace_for_all_lengths(hq, hkv, hd, q, longest):
         c.kv_len = torch.arange(n - q + 1, n + 1, dtype=torch.int32, device=DEV)
         ws.fill_(0xFF)
         assert torch.equal(c.run(workspace=ws, max_kv_len=n), c.run(max_kv_len=n)), n
+
+
+@pytest.mark.parametrize("hd,power", [(64, 66), (64, 80), (128, 97), (128, -20), (256, -40)])
+def test_write_far_from_one(hd, power):
+    """bf16 heads whose squares are past fp32's range (above 2^64), and small ones: K's codes bit for bit."""
+    hkv, m = 2, 12
+    g = gen(hd + power)
+    qkv = (randn((m, 3 * hkv * hd), g) * 2.0 ** power).bfloat16()
+    kw = (1 + 0.2 * randn((hd,), g)).bfloat16()
+    cos, sin = rope_tables(64, hd)
+    c = Cache(m, hkv, hd, (0.0019, 0.002))
+    pos = torch.arange(m, dtype=torch.int32, device=DEV)
+    write(c, qkv, None, kw, cos, sin, pos, hkv)
+    k = P.norm_rope(qkv.view(m, 3 * hkv, hd)[:, hkv:2 * hkv], kw, cos[:m], sin[:m], 1e-6).float()
+    if power > 0:
+        assert (k.abs().amax((1, 2)) > 1).all()  # (normed: of ordinary size)
+    codes, sf = P.quantise(k, c.scales[0])
+    assert torch.equal(P.sf_rows(c.ksf, m), sf) and torch.equal(c.k, codes)
