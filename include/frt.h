@@ -552,7 +552,9 @@ typedef enum { FRT_X_16BIT = 0, FRT_X_E4M3 = 1, FRT_X_E4M3_BLOCK = 2, FRT_X_NVFP
  * x as the 16-bit type or as this library's FP8 / NVFP4 ops wrote it.  Products
  * are exact, sums fp32, one rounding to 16 bits.  (bf16 rows are carried as
  * fp16 times a power of two per row and 128 columns: exact down to 2^-28 of the
- * block's largest magnitude, and below that to 2^-39 of it.)  A NaN scale factor
+ * block's largest magnitude, and below that to 2^-39 of it, or to 2^-151 /
+ * w_scale where that is more.  Products of the scales x_scales and w_scale are
+ * formed in fp32: one below 2^-126 keeps fewer bits.)  A NaN scale factor
  * of row n of w makes column n of y NaN.  No atomics: the same call gives the
  * same bits.
  *

@@ -57,12 +57,16 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   return d;
 }
 // Power of two that brings magnitude amax (> 0, finite) into [2^14, 2^15), at
-// most 2^127 (below 2^-113 the bf16 numbers, multiples of 2^-133, are exact in
-// binary16 all the same); 1 for zero, infinite and NaN amax.
-__device__ __forceinline__ float pow2_to_half_range(float amax) {
+// most 2^most (with 127: below 2^-113 the bf16 numbers, multiples of 2^-133, are
+// exact in binary16 all the same); 1 for zero, infinite and NaN amax.
+__device__ __forceinline__ float pow2_to_half_range(float amax, int most = 127) {
   const int e = (int)(__float_as_uint(amax) >> 23) - 127;  // amax >= 0; subnormals count as 2^-127
   if (!(amax > 0.0f) || e == 128) return 1.0f;
-  return __int_as_float((min(14 - e, 127) + 127) << 23);  // (14 - e >= -113)
+  return __int_as_float((min(14 - e, most) + 127) << 23);  // (14 - e >= -113)
+}
+// The largest power for which `scale` divided by it is a normal number.
+__device__ __forceinline__ int most_pow2(float scale) {
+  return min((int)(__float_as_uint(scale) >> 23 & 0xFF) - 1, 127);
 }
 
 }  // namespace frt

@@ -22,7 +22,9 @@
 // (16 bytes are a lane's part of two products).  FP16 rows, e4m3 codes and
 // NVFP4 code * factor are exact there.  bf16 rows are scaled by a power of two
 // per row and group, and like the block-scaled FP8 rows keep a factor per row
-// and group that is applied to the group's fp32 sums.
+// and group that is applied to the group's fp32 sums.  That factor, w_scale over
+// the power of two, is kept a normal number: for tiny groups the power is smaller
+// and binary16 cuts x at 2^-151 / w_scale, which is below 2^-139 in y.
 #include <algorithm>
 
 #include "matvec_nvfp4.cuh"
@@ -174,7 +176,7 @@ __device__ __forceinline__ void stage_x(const Args& a, int seg, int len, int n_r
           float2 f[4];
           unpack_pairs<FRT_BF16, 4>(&o.x, f);
           const float amax = fmaxf(absmax4(f[0].x, f[0].y, f[1].x, f[1].y), absmax4(f[2].x, f[2].y, f[3].x, f[3].y));
-          const float s = pow2_to_half_range(half_warp_max_abs(amax));
+          const float s = pow2_to_half_range(half_warp_max_abs(amax), most_pow2(w_scale));
           mul_pairs<4>(f, s);
           pack_pairs<FRT_F16, 4>(f, &o.x);
           scale[b] = 1.0f / s;

@@ -82,15 +82,16 @@ struct XRow {
     return o;
   }
 };
-// The same as binary16; 16 lanes hold a group of a row.
+// The same as binary16; 16 lanes hold a group of a row.  `most`: most_pow2 of the
+// weights' scale.
 template <XForm FORM>
-__device__ __forceinline__ uint4 convert_x(RawX& raw) {
+__device__ __forceinline__ uint4 convert_x(RawX& raw, int most) {
   uint4 o = raw.v;
   if (FORM == kXScaled16) {
     float2 f[4];
     unpack_pairs<FRT_BF16, 4>(&o.x, f);
     const float amax = fmaxf(absmax4(f[0].x, f[0].y, f[1].x, f[1].y), absmax4(f[2].x, f[2].y, f[3].x, f[3].y));
-    const float s = pow2_to_half_range(half_warp_max_abs(amax));
+    const float s = pow2_to_half_range(half_warp_max_abs(amax), most);
     mul_pairs<4>(f, s);
     pack_pairs<FRT_F16, 4>(f, &o.x);
     raw.scale = 1.0f / s;
@@ -166,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) load_w(w[u]);  // constant inputs: before the wait
   const float w_scale = __ldg(a.w_scale);
+  const int most = most_pow2(w_scale);
   if (threadIdx.x == 0) {
     mbar_init(&bar[0], 1);
     mbar_init(&bar[1], 1);
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const MatvecArgs a, 
 #pragma unroll
       for (int n = 0; n < kXEach; ++n) {
         const int r = h + 32 * n;
-        const uint4 v = convert_x<FORM>(x[n]);
+        const uint4 v = convert_x<FORM>(x[n], most);
         st_shared16(to_b + (l >> 3) * (NX * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4), v);
         if (kScaled && l == 0) xs[u * NX + r] = x[n].scale * w_scale;
         x[n] = x_row[n].next(a, r < a.rows && k_left > 0);

@@ -931,3 +931,19 @@ def test_write_far_from_one(hd, power):
         assert (k.abs().amax((1, 2)) > 1).all()  # (normed: of ordinary size)
     codes, sf = P.quantise(k, c.scales[0])
     assert torch.equal(P.sf_rows(c.ksf, m), sf) and torch.equal(c.k, codes)
+
+
+@pytest.mark.parametrize("m", [4, 14, 40, 100])
+@pytest.mark.parametrize("power,shrink", [(-118, 1.0), (-110, 2.0 ** -8), (-90, 2.0 ** -30), (100, 2.0 ** -30)])
+def test_matvec_small_rows_and_small_weights(m, power, shrink):
+    """bf16 rows and weights whose factors together leave fp32's normal range, though y does not."""
+    g = gen(m + power)
+    n, k = 70, 272
+    wc, wsf, ws, w = weights(n, k, g, "rows")
+    ws, w = ws * shrink, w * shrink
+    x = (randn((m, k), g) * 2.0 ** power).bfloat16()
+    y = torch.empty((m, n), dtype=torch.bfloat16, device=DEV)
+    frt.frt_matvec_nvfp4(x, wc, wsf, ws, y)
+    ref = x.double() @ w.t()
+    assert (ref.abs().median() > 2.0 ** -126).all()
+    assert ((y.double() - ref).abs() <= P.matvec_bound(x.double(), w, ref, torch.bfloat16)).all()
