@@ -56,12 +56,13 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// Power of two that brings magnitude amax (> 0, finite) into [2^14, 2^15), at
-// most 2^most (with 127: below 2^-113 the bf16 numbers, multiples of 2^-133, are
-// exact in binary16 all the same); 1 for zero, infinite and NaN amax.
+// Power of two that brings magnitude amax (> 0) into [2^14, 2^15), at most 2^most
+// (with 127: below 2^-113 the bf16 numbers, multiples of 2^-133, are exact in
+// binary16 all the same); 1 for zero and NaN amax.  Beside an infinity the finite
+// numbers stay finite.
 __device__ __forceinline__ float pow2_to_half_range(float amax, int most = 127) {
-  const int e = (int)(__float_as_uint(amax) >> 23) - 127;  // amax >= 0; subnormals count as 2^-127
-  if (!(amax > 0.0f) || e == 128) return 1.0f;
+  const int e = min((int)(__float_as_uint(amax) >> 23) - 127, 127);  // amax >= 0; subnormals count as 2^-127
+  if (!(amax > 0.0f)) return 1.0f;
   return __int_as_float((min(14 - e, most) + 127) << 23);  // (14 - e >= -113)
 }
 // The largest power for which `scale` divided by it is a normal number.

@@ -947,3 +947,27 @@ def test_matvec_small_rows_and_small_weights(m, power, shrink):
     ref = x.double() @ w.t()
     assert (ref.abs().median() > 2.0 ** -126).all()
     assert ((y.double() - ref).abs() <= P.matvec_bound(x.double(), w, ref, torch.bfloat16)).all()
+
+
+@pytest.mark.parametrize("m", [3, 12, 40])
+@pytest.mark.parametrize("beside", [-1e6, -3e38])
+def test_matvec_infinity_beside_large_numbers(m, beside):
+    """An infinite element of a bf16 row gives infinities of its product's sign (NaN where the weight is zero),
+    whatever finite numbers stand beside it."""
+    g = gen(m)
+    wc, wsf, ws, w = weights(90, 256, g, "rows")
+    x = randn((m, 256), g).bfloat16()
+    x[1, 7] = float("inf")
+    x[1, 8:40] = beside
+    x[2, 200] = float("-inf")
+    x[2, 190:199] = -beside
+    y = torch.empty((m, 90), dtype=torch.bfloat16, device=DEV)
+    frt.frt_matvec_nvfp4(x, wc, wsf, ws, y)
+    ref = x.double() @ w.t()
+    for r in (1, 2):
+        assert torch.isinf(ref[r]).any()
+        assert torch.equal(torch.isnan(y[r]), torch.isnan(ref[r]))
+        fine = ~torch.isnan(ref[r])
+        assert torch.equal(y[r][fine].double(), ref[r][fine])
+    rest = [r for r in range(m) if r not in (1, 2)]
+    assert ((y[rest].double() - ref[rest]).abs() <= P.matvec_bound(x[rest].double(), w, ref[rest], torch.bfloat16)).all()
