@@ -541,15 +541,18 @@ frt_status launch_few(const Args& a, cudaStream_t stream) {
                         : launch_layout<4, SCALED>(a, stream);
 }
 // Up to kFewRows rows of x the warps' products win: 16 rows of 4096 to 32768
-// 23.5-32 us against the tiles' 53-64, of 8192 to 8192 16-19 against 28-33, of
-// 4096 to 1024 6.4-8.2 against 7.4-7.5 (the forms of x).  Up to kMoreRows, which is
-// what they carry at most, they win where the weights are many: 32 rows of 4096
-// to 32768 35-46 against 54-65, of 2048 to 16384 13-15.4 against 15-16.8, of 4096
-// to 4096 11.1-11.9 against 10.9-11.3, of 256 to 11682 4.6-5.0 against 3.9-4.0.
+// 23.5-32 us against the tiles' 53-64 (the forms of x), of 8192 to 8192 16-19
+// against 28-33, of 1024 to 4096 3.9-4.4 against 5.3-5.8, of 4096 to 1024 6.2-6.6
+// against 6.9-7.5, where only bf16 rows take 8.0 against 7.5.  Up to kMoreRows,
+// which is what they carry at most, they win where the weights are more than
+// kManyWeights: 32 rows of 4096 to 32768 35-46 against 54-65, of 5120 to 5120
+// 13.6-15.9 against 18.2-21.6, of 2048 to 16384 13.1-15.4 against 14.9-17.1; at
+// kManyWeights, 4096 to 4096, 17 rows 10.2-11.3 against 10.5-11.2 and 32 rows
+// 10.9-12.2 against 10.6-11.4; of 256 to 11682 4.6-5.0 against 3.9-4.0.
 constexpr int kFewRows = 16, kMoreRows = 32;
 constexpr int64_t kManyWeights = 1 << 24;
 bool warps_win(const Args& a) {
-  return a.rows <= kFewRows || (a.rows <= kMoreRows && (int64_t)a.N * a.K >= kManyWeights);
+  return a.rows <= kFewRows || (a.rows <= kMoreRows && (int64_t)a.N * a.K > kManyWeights);
 }
 constexpr int kMaxSize = 0x7FFF0000;  // (32-bit indices reach past M, N and K by less than 65536)
 frt_status launch_rows(Args a, cudaStream_t stream) {

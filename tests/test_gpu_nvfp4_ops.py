@@ -971,3 +971,22 @@ def test_matvec_infinity_beside_large_numbers(m, beside):
         assert torch.equal(y[r][fine].double(), ref[r][fine])
     rest = [r for r in range(m) if r not in (1, 2)]
     assert ((y[rest].double() - ref[rest]).abs() <= P.matvec_bound(x[rest].double(), w, ref[rest], torch.bfloat16)).all()
+
+
+@pytest.mark.parametrize("m,n,k,tiles", [(16, 64, 4096, False), (17, 64, 4096, True), (32, 4096, 4096, True),
+                                         (32, 4112, 4096, False), (33, 4112, 4096, True)])
+def test_matvec_which_kernel(m, n, k, tiles):
+    """Which kernel a shape takes: the one for many rows gives up its waits without polls and writes NaN, the other
+    has none."""
+    prev = frt.frt_get_wait_polls()
+    try:
+        frt.frt_set_wait_polls(0)
+        y, ref, tol = matvec_case(m, n, k, "16", dt="f16", seed=m)
+        torch.cuda.synchronize()
+    finally:
+        frt.frt_set_wait_polls(prev)
+    if tiles:
+        assert torch.isnan(y).all()
+    else:
+        assert ((y.double() - ref).abs() <= tol).all()
+    check_matvec(m, n, k, "16", dt="f16", seed=m)
