@@ -366,6 +366,9 @@ def _entry(name):
             raise FrtError("load", -1, "%s is missing; build it with `python -m memory_bound_non_b200.build`" %
                            MARSHAL_PATH)
         from . import _marshal as module
+        if module.built_for != torch.__version__:
+            raise FrtError("load", -1, "%s was built against torch %s, not %s; build it again with `python -m "
+                           "memory_bound_non_b200.build`" % (MARSHAL_PATH, module.built_for, torch.__version__))
         module.set_error(FrtError)
         _native = module
     addresses = load().addresses

@@ -23,6 +23,7 @@ LIB = os.path.join(PKG, "libfrt.so")
 DEBUG_LIB = os.path.join(PKG, "libfrt_debug.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 MARSHAL_LIB = os.path.join(PKG, "_marshal.so")
+MARSHAL_TAG = os.path.join(PKG, "_marshal.tag")  # what _marshal.so was built against
 DEBUG_FLAGS = ["-rdc=true", "-DFRT_DEBUG_BOUNDS"]
 
 NVCC_FLAGS = [
@@ -87,11 +88,24 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     return lib
 
 
+def _marshal_built_for() -> str:
+    import torch
+    return "torch %s, %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
+def marshal_stale() -> bool:
+    """_marshal.so is missing, older than its sources, or built against another torch or Python."""
+    deps = [MARSHAL_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not os.path.exists(MARSHAL_LIB) or not os.path.exists(MARSHAL_TAG) or \
+            any(os.path.getmtime(d) > os.path.getmtime(MARSHAL_LIB) for d in deps):
+        return True
+    with open(MARSHAL_TAG) as f:
+        return f.read() != _marshal_built_for()
+
+
 def build_marshal(force: bool = False) -> str:
     """Compile _marshal.so against the installed torch and CUDA headers."""
-    deps = [MARSHAL_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(MARSHAL_LIB) and \
-            all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL_LIB) for d in deps):
+    if not force and not marshal_stale():
         return MARSHAL_LIB
     import torch
     torch_dir = os.path.dirname(torch.__file__)
@@ -102,10 +116,14 @@ def build_marshal(force: bool = False) -> str:
     tmp = MARSHAL_LIB + ".tmp.%d" % os.getpid()
     subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w"] +
                    [a for d in include for a in ("-I", d)] + [MARSHAL_SRC, "-o", tmp,
+                    '-DFRT_BUILT_FOR="%s"' % torch.__version__,
                     "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
                     "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
                     "-ltorch_python"], check=True)
     os.replace(tmp, MARSHAL_LIB)
+    with open(MARSHAL_TAG + ".tmp.%d" % os.getpid(), "w") as f:
+        f.write(_marshal_built_for())
+    os.replace(f.name, MARSHAL_TAG)
     return MARSHAL_LIB
 
 

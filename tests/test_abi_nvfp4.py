@@ -155,3 +155,19 @@ def test_attn_workspace_never_falls_with_the_length(hq, hkv, hd, n_seqs, q):
         last = size
         if n % 4096 == 0:
             assert W(1, n_seqs, hq, hkv, hd, q, n) <= size <= W(2 * q * n_seqs, n_seqs, hq, hkv, hd, q, n)
+
+
+def test_marshalling_is_built_again_for_another_torch(monkeypatch, tmp_path):
+    """_marshal.so holds torch's own layouts: one built against another torch is stale, and is not loaded."""
+    from memory_bound_non_b200 import build as B
+    B.build_marshal()
+    assert not B.marshal_stale()
+    tag = tmp_path / "tag"
+    monkeypatch.setattr(B, "MARSHAL_TAG", str(tag))
+    assert B.marshal_stale()
+    tag.write_text("torch 1.0, cpython-312")
+    assert B.marshal_stale()
+    monkeypatch.setattr(frt, "_native", None)
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    with pytest.raises(frt.FrtError, match="built against"):
+        frt._entry("frt_matvec_nvfp4")
