@@ -120,3 +120,15 @@ def matvec_bound(x, w, ref, dt, group=128):
     half_step = torch.finfo(dt).eps / 2
     return (K + 8) * 2.0 ** -23 * mag + 2.0 ** -39 * (top @ w.abs().t()) + 1.01 * half_step * ref.abs() + \
         torch.finfo(dt).smallest_normal * half_step
+
+
+def attention_norm_bound(smax, hd, depth, dt):
+    """Bound on |out - ref| / |ref| as norms over a head's outputs, for values v that are independent of the scores
+    (zero-mean, one variance).  With weights p fixed, ref = sum p v / sum p has the expected square sum p^2 / (sum p)^2
+    and an error sum d p v / sum p of relative weight errors |d| <= D has at most D^2 times that, so their norms'
+    ratio is D, and the common error of the denominator adds another D.  D is half a binary16 step, the exponential's
+    2^-22, the score's (hd + 2) 2^-23 smax, and 2^-23 for each of the `depth` additions that follow one another in a
+    sum.  The result adds half a step of its type.  Both norms are of hd numbers or more: they are off their expectations by
+    1 / sqrt(2 hd), far inside the factor of 2."""
+    d = 2.0 ** -11 + 2.0 ** -22 + (hd + 2) * 2.0 ** -23 * smax + depth * 2.0 ** -23
+    return 2 * (2 * d + torch.finfo(dt).eps / 2)

@@ -1,0 +1,142 @@
+"""Paths of the attention over the NVFP4 cache: which kernel a shape takes, keys cut into parts that a second kernel
+joins (with bounds and inputs that show every part), workspaces on streams other than the current one."""
+import pytest
+import torch
+
+import memory_bound_non_b200 as frt
+import nvfp4_plain as P
+from test_gpu_nvfp4_ops import DEV, DT, Case
+
+pytestmark = pytest.mark.gpu
+
+
+def takes_tiles(c, **kw):
+    """Does the call take the kernel for many rows?  Without polls it gives up its waits and reports bit 1; the kernel
+    for few rows has no waits."""
+    prev = frt.frt_get_wait_polls()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    try:
+        frt.frt_set_wait_polls(0)
+        c.run(status=status, **kw)
+        torch.cuda.synchronize()
+    finally:
+        frt.frt_set_wait_polls(prev)
+    return bool(status.item() & 2)
+
+
+def takes_join(c, **kw):
+    """Are the keys cut into parts that a second kernel joins?  Only such a call needs a workspace."""
+    try:
+        c.run(workspace=torch.empty(16, dtype=torch.uint8, device=DEV), **kw)
+    except frt.FrtError as e:
+        assert e.status == frt.FRT_ERR_INVALID_ARG
+        return True
+    torch.cuda.synchronize()
+    return False
+
+
+def check_norms(c, out):
+    """The error of each head as a norm: see attention_norm_bound."""
+    n = sum(c.tokens)
+    k, v = c.cache.values("k"), c.cache.values("v")
+    ref, _, smax = P.attention(c.q[:n], k, v, c.spans(), c.slots, c.scale, lambda h: h // (c.hq // c.hkv))
+    # a warp's (or CTA's) keys follow one another in its sums, then warps and parts
+    bound = P.attention_norm_bound(smax, c.hd, c.longest / 8 + 128, DT[c.dt])
+    err, size = (out[:n].double() - ref).norm(dim=-1), ref.norm(dim=-1)
+    assert (err <= bound * size).all(), float((err / (bound * size)).max())
+
+
+MANY = [([300], [1200], 16, 1, 64, {}), ([300], [1200], 16, 2, 64, {}), ([700], [1500], 5, 5, 80, {}),
+        ([500], [1500], 6, 2, 96, {}), ([200], [900], 16, 8, 128, {}), ([300], [900], 7, 1, 192, {}),
+        ([200], [900], 8, 1, 256, {}), ([400, 3, 0, 200], [900, 700, 5, 190], 16, 2, 64, dict(page=16)),
+        ([300], [1200], 16, 1, 128, dict(page=64, window=33)), ([41], [8192], 8, 1, 256, {})]
+FEW = [([1], [60000], 8, 1, 64, {}), ([10], [978], 8, 1, 256, {}), ([47], [137], 4, 2, 128, {}), ([1], [50001], 4, 2, 128, {}),
+       ([41], [600], 8, 1, 256, {})]
+
+
+@pytest.mark.parametrize("tiles,case", [(True, c) for c in MANY] + [(False, c) for c in FEW])
+def test_attn_which_kernel(tiles, case):
+    tokens, lens, hq, hkv, hd, kw = case
+    assert takes_tiles(Case(tokens, lens, hq, hkv, hd, **kw)) == tiles
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("page,window", [(0, 0), (16, 0), (0, 3000), (20, 5000)])
+@pytest.mark.parametrize("tokens,hq,hkv,hd,n", [(41, 8, 1, 256, 8192), (12, 32, 4, 128, 12001), (100, 4, 4, 64, 20003)])
+def test_attn_many_rows_joined(tokens, hq, hkv, hd, n, page, window, dt):
+    """The kernel for many rows over a long prefix: its parts joined by the second kernel."""
+    c = Case([tokens], [n], hq, hkv, hd, dt, page=page, window=window, seed=tokens)
+    assert takes_tiles(c) and takes_join(c)
+    out = c.check()
+    check_norms(c, out)
+    assert torch.equal(out, c.run())
+
+
+def test_attn_many_rows_joined_batch():
+    """Sequences of different lengths, one without keys and one without tokens, in parts."""
+    c = Case([50, 0, 60], [12001, 40, 37], 8, 1, 128, page=16, extra_tokens=3)
+    assert takes_tiles(c) and takes_join(c)
+    check_norms(c, c.check())
+    c = Case([50, 49], [12001, 0], 8, 1, 128, page=16, causal=False)
+    assert takes_tiles(c) and takes_join(c)
+    assert (c.check()[50:] == 0).all()
+
+
+@pytest.mark.parametrize("hq,hkv,hd,n,page,q", [(8, 1, 64, 60000, 0, 1), (4, 2, 128, 50001, 20, 1), (8, 8, 256, 20011, 16, 1),
+                                                (40, 2, 128, 33000, 64, 1), (32, 8, 128, 131072, 0, 1), (6, 2, 192, 70000, 0, 2),
+                                                (8, 2, 80, 40000, 0, 3)])
+def test_attn_long_norms(hq, hkv, hd, n, page, q):
+    """Long calls of the kernel for few rows, joined: an error that a part of the keys, lost or weighed wrongly, would
+    exceed (test_nvfp4_bounds plants such)."""
+    c = Case([q], [n], hq, hkv, hd, page=page, seed=n)
+    assert not takes_tiles(c) and takes_join(c)
+    check_norms(c, c.run())
+
+
+@pytest.mark.parametrize("tokens,hq,hkv,hd,n,page", [(1, 8, 1, 64, 60000, 0), (1, 4, 2, 128, 50001, 20), (1, 8, 8, 256, 20011, 16),
+                                                     (1, 32, 8, 128, 131072, 0), (2, 6, 2, 192, 70000, 0),
+                                                     (41, 8, 1, 256, 8192, 0), (100, 4, 4, 64, 20003, 16),
+                                                     (10, 8, 1, 256, 978, 0), (1, 8, 8, 128, 3000, 16)])
+def test_attn_every_part_counts(tokens, hq, hkv, hd, n, page):
+    """Equal scores (K is zero), and V zero but for one position of each dimension, spread over the whole length: every
+    output is that value over n.  A part that is lost, doubled or weighed wrongly changes all outputs by its share of
+    the keys, a position that is lost its own."""
+    c = Case([tokens], [n], hq, hkv, hd, page=page, causal=False, seed=n)
+    c.cache.scales.fill_(1.0)
+    c.cache.k.zero_()
+    c.cache.v.zero_()
+    c.cache.ksf.fill_(0x38)  # 1
+    c.cache.vsf.fill_(0x7E)  # 448
+    pos = (torch.arange(hd, device=DEV) * (n - 1)) // (hd - 1)  # the first and the last among them
+    slots = c.slots(0, pos)
+    for d in range(hd):
+        c.cache.v[slots[d], :, d // 2] |= 7 << 4 * (d % 2)  # 6
+    out = c.run()
+    want = 2688.0 / n
+    # weights of 2^11, their sums exact in fp32 below 2^24 of them; the reciprocal, two products, half a step of the result
+    tol = want * (2.0 ** -21 + torch.finfo(out.dtype).eps / 2)
+    assert ((out.double() - want).abs() <= tol).all()
+
+
+def test_attn_on_another_stream():
+    """Calls on streams that are not the current one, with a workspace of their own allocation each: it belongs to
+    that stream, so that memory taken on the current stream meanwhile is not the same."""
+    cases = [Case([1], [60000], 8, 1, 64, seed=s) for s in (1, 2)] + [Case([41], [8192], 8, 1, 256)]
+    refs = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    sizes = [frt.attn_nvfp4_workspace(c.q, c.hkv, c.longest, max_q_len=len(c.seq)).numel() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        outs = [torch.full_like(r, 9.0) for r in refs]
+        torch.cuda.synchronize()
+        for c, st, o in zip(cases, streams, outs):
+            with torch.cuda.stream(st):
+                torch.cuda._sleep(20000000)  # the call's kernels start after what follows here
+            frt.frt_attn_nvfp4_kvcache(c.q, *c.cache.args, c.kv_len, o, c.scale, max_kv_len=c.longest, stream=st)
+        taken = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(4)]
+        for st in streams:
+            st.synchronize()
+        torch.cuda.synchronize()
+        for o, r in zip(outs, refs):
+            assert torch.equal(o, r)
+        assert all((t == 0xFF).all() for t in taken)
