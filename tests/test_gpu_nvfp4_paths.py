@@ -1,5 +1,7 @@
 """Paths of the attention over the NVFP4 cache: which kernel a shape takes, keys cut into parts that a second kernel
 joins (with bounds and inputs that show every part), workspaces on streams other than the current one."""
+import math
+
 import pytest
 import torch
 
@@ -140,3 +142,27 @@ def test_attn_on_another_stream():
         for o, r in zip(outs, refs):
             assert torch.equal(o, r)
         assert all((t == 0xFF).all() for t in taken)
+
+
+@pytest.mark.parametrize("bits", [20, 23, 24, 25])
+@pytest.mark.parametrize("tokens,hq,hd,n", [(2400, 16, 64, 131072), (2400, 16, 128, 131072), (1200, 16, 256, 131072),
+                                            (2400, 16, 64, 524288), (1, 8, 64, 131072), (400, 4, 128, 131072)])
+def test_attn_one_key_above_a_long_tail(tokens, hq, hd, n, bits):
+    """One key whose weight is 2^bits times that of every other; V is zero there and one elsewhere.  The output is the
+    tail's share of the sum of the weights.  All weights are powers of two (2^11 and 2^(11 - bits)), so products and the
+    tail's sum are exact in fp32; a sum that takes the weights one by one would lose all those of half its step or
+    less, n 2^-24 of it."""
+    q = torch.ones((tokens, hq, hd), device=DEV, dtype=torch.float16)
+    one = torch.full(frt.nvfp4_kv_sf_shape(n, 1, hd), 0x38, device=DEV, dtype=torch.uint8)
+    scales = torch.ones(2, device=DEV)
+    kv_len = torch.full((tokens,), n, device=DEV, dtype=torch.int32)
+    out = torch.empty_like(q)
+    for at in (0, n // 3):
+        k = torch.zeros((n, 1, hd // 2), device=DEV, dtype=torch.uint8)
+        v = torch.full((n, 1, hd // 2), 0x22, device=DEV, dtype=torch.uint8)  # 1.0
+        k[at], v[at] = 0x22, 0
+        frt.frt_attn_nvfp4_kvcache(q, k, one, v, one, scales, kv_len, out, bits * math.log(2) / hd)
+        tail = (n - 1) * 2.0 ** -bits
+        want = tail / (1 + tail)
+        # half a step of the result, and 2^-20 for the exponential, the division and the rescaling of the sums
+        assert ((out.double() - want).abs() <= want * (2.0 ** -11 + 2.0 ** -20)).all(), (at, float(out[0, 0, 0]), want)
