@@ -481,7 +481,7 @@ frt_status launch_one(Args a, cudaStream_t stream) {
   // and 0.2 (1 + kw) for every turn of a warp.
   double best = 0;
   size_t smem = 0;
-  int per_sm = 1;
+  int64_t grid_ctas = 1;  // (or clusters) that run at once: the sums' place in shared memory goes by it
   a.cluster = 0;
   for (int ranks = 1; ranks <= 8; ranks *= 2) {
     if (ranks > 1 && ranks > a.groups) break;
@@ -514,7 +514,7 @@ frt_status launch_one(Args a, cudaStream_t stream) {
           a.kw = kw;
           a.kw_log2 = log2;
           a.seg_groups = seg;
-          per_sm = sm;
+          grid_ctas = used;
           smem = red + seg * group_bytes;
         }
       }
@@ -524,8 +524,7 @@ frt_status launch_one(Args a, cudaStream_t stream) {
   static SmemOptIn opted;
   const frt_status st = opt_in_smem(matvec_kernel<NT, SCALED, LAY>, smem, opted);
   if (st != FRT_OK) return st;
-  const int ctas = cluster_room(per_sm, a.cluster);
-  const dim3 grid((unsigned)((a.tiles < ctas ? a.tiles : ctas) * a.cluster)), block(32 * kWarps);
+  const dim3 grid((unsigned)(grid_ctas * a.cluster)), block(32 * kWarps);
   if (a.cluster > 1) return launch_cluster(matvec_kernel<NT, SCALED, LAY>, grid, block, smem, stream, a.cluster, a);
   return launch(matvec_kernel<NT, SCALED, LAY>, grid, block, smem, stream, a);
 }
