@@ -486,6 +486,10 @@ frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8_t* k_sf, c
  *   rounded to fp16 (scaled so that weights down to 2^-25 of the row's largest
  *   keep 11 bits) and their sum is the sum of the rounded ones; the output is
  *   rounded once to 16 bits.  No atomics: the same call gives the same bits.
+ *   (bf16 q rows are carried as fp16 times a power of two per row: exact down to
+ *   2^-28 of the row's largest magnitude, and below that to 2^-39 of it.   The
+ *   output sums are the tensor cores': a weight below 2^-22 of its row's sum keeps
+ *   some of its bits there only, about 2^-24 of max |v| lost for each at most.)
  *
  *   q, out        device [M, Hq, hd] 16-bit, 16-byte aligned.
  *   codes, sf, kv_scales   the cache, as above.
@@ -611,9 +615,10 @@ frt_status frt_copy_rows(const void* src, void* dst, int rows, int row_bytes, cu
  * inputs (static_scale, kv_scales, global_scale), and the matrix-vector
  * product's weights -- may be read before that
  * wait, so they must not be written by the kernel launched just before it on
- * the same stream (no kernel of this library writes them; a host copy or a
- * kernel further back is fine: a kernel is scheduled early only once every
- * CTA of its predecessor has passed its own wait).  Results are identical
+ * the same stream (of this library's kernels only the NVFP4 producers could,
+ * where their output serves as weights; a host copy or a kernel further back is
+ * fine: a kernel is scheduled early only once every CTA of its predecessor has
+ * passed its own wait).  Results are identical
  * either way.  The switch is process-wide and read at each launch; changing
  * it while another thread launches affects only later launches.
  */

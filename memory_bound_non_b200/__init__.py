@@ -16,6 +16,14 @@ Functions carry the C names of ``include/frt.h``:
     frt_noop(grid, block), frt_copy_rows(src, dst)      (launch-floor probes)
     frt_set_pdl / frt_get_pdl, frt_set_wait_polls / frt_get_wait_polls
 
+Constant inputs.  Launches overlap the kernel before them on the stream
+(``frt_set_pdl``), and what does not change from step to step is read without
+waiting for it: norm weights, RoPE tables, op (b)'s positions, scales, and
+frt_matvec_nvfp4's weights with their factors, scale and bias.  The kernel
+launched just before, torch's too, must not write these.  Where it does (weights
+quantised, or a scale computed, right before the call), synchronise in between
+once, or turn the overlap off with ``frt_set_pdl(False)`` for that call.
+
 ``load_debug()`` opens the bounds-checked build (libfrt_debug.so,
 include/frt_debug.h); ``using_library(load_debug())`` routes these functions
 through it and ``bounds_violations()`` reads and clears its counter.
@@ -380,7 +388,9 @@ def frt_qkv_norm_rope_nvfp4_kvcache(qkv, q_norm_w, k_norm_w, cos_tab, sin_tab, p
                                     stream=None):
     """Op (b) with an NVFP4 KV cache: codes uint8 [capacity, Hkv, hd/2], sf uint8
     nvfp4_kv_sf_shape(capacity, Hkv, hd), kv_scales fp32[2] (global scales of K
-    and V).  slots int32 [M] (-1: skip the row) or None (slot = position)."""
+    and V).  slots int32 [M] (-1: skip the row) or None (slot = position).
+    The norm weights, tables and kv_scales are constant inputs (see the module's
+    docstring); positions and slots may come from the kernel just before."""
     m, fn, text = _entry("frt_qkv_norm_rope_nvfp4_kvcache")
     m.write(fn, text, qkv, q_norm_w, k_norm_w, cos_tab, sin_tab, positions, slots, q_out, k_codes, k_sf, v_codes, v_sf,
             kv_scales, status, Hq, Hkv, hd, eps, stream)
@@ -388,7 +398,8 @@ def frt_qkv_norm_rope_nvfp4_kvcache(qkv, q_norm_w, k_norm_w, cos_tab, sin_tab, p
 
 def frt_nvfp4_kvcache_read(k_codes, k_sf, v_codes, v_sf, kv_scales, slots, k_out, v_out, status=None, stream=None):
     """Slots of an NVFP4 KV cache back in 16 bits: k_out, v_out [n, Hkv, hd];
-    slots int32 [n] or None (slots 0 .. n-1)."""
+    slots int32 [n] or None (slots 0 .. n-1).  kv_scales is a constant input
+    (see the module's docstring)."""
     m, fn, text = _entry("frt_nvfp4_kvcache_read")
     m.read(fn, text, k_codes, k_sf, v_codes, v_sf, kv_scales, slots, k_out, v_out, status, stream)
 
@@ -428,7 +439,12 @@ def frt_matvec_nvfp4(x, w_codes, w_sf, w_scale, y, bias=None, x_format="16", x_s
     """y [M, N] = x w^T + bias with NVFP4 weights (w_codes uint8 [N, K/2], w_sf in
     sf_layout, w_scale fp32[1]).  x: 16-bit [M, K]; "e4m3" / "e4m3_block" uint8
     [M, K] with x_scales fp32 [1] / [M, ceil(K/128)]; "nvfp4" uint8 [M, K/2] with
-    x_sf in sf_layout and x_scales fp32[1]."""
+    x_sf in sf_layout and x_scales fp32[1].
+
+    w_codes, w_sf, w_scale and bias are constant inputs: the kernel launched just
+    before this call on its stream must not write them.  After quantising weights
+    synchronise once before the first product (or call frt_set_pdl(False) around
+    it); x, x_scales and x_sf may come from the kernel just before."""
     m, fn, text = _entry("frt_matvec_nvfp4")
     if x_format not in X_FORMAT or sf_layout not in SF_LAYOUT:
         raise FrtError("frt_matvec_nvfp4", FRT_ERR_INVALID_ARG,
