@@ -487,7 +487,7 @@ frt_status frt_nvfp4_kvcache_read(const uint8_t* k_codes, const uint8_t* k_sf, c
  *   keep 11 bits) and their sum is the sum of the rounded ones; the output is
  *   rounded once to 16 bits.  No atomics: the same call gives the same bits.
  *   (bf16 q rows are carried as fp16 times a power of two per row: exact down to
- *   2^-28 of the row's largest magnitude, and below that to 2^-39 of it.   The
+ *   2^-28 of the row's largest magnitude, and below that to 2^-39 of it.  The
  *   output sums are the tensor cores': a weight below 2^-22 of its row's sum keeps
  *   some of its bits there only, about 2^-24 of max |v| lost for each at most.)
  *

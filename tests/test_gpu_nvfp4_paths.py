@@ -7,7 +7,7 @@ import torch
 
 import memory_bound_non_b200 as frt
 import nvfp4_plain as P
-from test_gpu_nvfp4_ops import DEV, DT, Case
+from test_gpu_nvfp4_ops import DEV, DT, Case, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,38 @@ def test_attn_one_key_above_a_long_tail(tokens, hq, hd, n, bits):
         want = tail / (1 + tail)
         # half a step of the result, and 2^-20 for the exponential, the division and the rescaling of the sums
         assert ((out.double() - want).abs() <= want * (2.0 ** -11 + 2.0 ** -20)).all(), (at, float(out[0, 0, 0]), want)
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 400])
+def test_cache_past_32_bits(tokens):
+    """A cache of more than 2^32 bytes a tensor: written, read back and attended to at its ends, through slots and
+    pages, by both attention kernels (one token, three, and many rows)."""
+    hkv, hd, hq, page = 8, 128, 16, 16
+    cap = 2 ** 23 + 2 ** 16
+    g = gen(tokens)
+    k, v = (torch.empty((cap, hkv, hd // 2), dtype=torch.uint8, device=DEV) for _ in range(2))
+    ksf, vsf = (torch.empty(frt.nvfp4_kv_sf_shape(cap, hkv, hd), dtype=torch.uint8, device=DEV) for _ in range(2))
+    scales = torch.tensor([0.002, 0.0021], device=DEV)
+    n = 2000
+    pages = torch.cat((torch.arange(cap // page - 100, cap // page), torch.arange(0, 100)))[torch.randperm(
+        200, generator=torch.Generator().manual_seed(1))][:n // page].int().to(DEV)
+    slots = (pages.long().repeat_interleave(page) * page + torch.arange(n, device=DEV) % page).int()
+    qkv = torch.randn((n, (hq + 2 * hkv) * hd), generator=g, device=DEV).half()
+    cos, sin = torch.ones((n, hd // 2), device=DEV), torch.zeros((n, hd // 2), device=DEV)
+    q = torch.empty((n, hq, hd), dtype=torch.float16, device=DEV)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    frt.frt_qkv_norm_rope_nvfp4_kvcache(qkv, None, None, cos, sin, pos, q, k, ksf, v, vsf, scales, hq, hkv, hd, slots=slots)
+    ko, vo = (torch.empty((n, hkv, hd), dtype=torch.float16, device=DEV) for _ in range(2))
+    frt.frt_nvfp4_kvcache_read(k, ksf, v, vsf, scales, slots, ko, vo)
+    heads = qkv.view(n, hq + 2 * hkv, hd)
+    values = []
+    for x, got, gs in ((heads[:, hq:hq + hkv], ko, scales[0]), (heads[:, hq + hkv:], vo, scales[1])):
+        codes, sf = P.quantise(x.float(), gs)
+        values.append(P.decode(codes, sf, gs))
+        assert torch.equal(got, values[-1].float().half())
+    out = torch.empty((tokens, hq, hd), dtype=torch.float16, device=DEV)
+    kv_len = torch.arange(n - tokens + 1, n + 1, dtype=torch.int32, device=DEV)
+    frt.frt_attn_nvfp4_kvcache(q[:tokens].contiguous(), k, ksf, v, vsf, scales, kv_len, out, 0.1, page_table=pages.view(1, -1),
+                               page_size=page, max_kv_len=n)
+    ref, vmax, smax = P.attention(q[:tokens], *values, [(0, int(m)) for m in kv_len], lambda i, p: p, 0.1, lambda h: h // 2)
+    assert ((out.double() - ref).abs() <= P.attention_bound(ref, vmax, smax, n, hd, torch.float16)).all()
