@@ -4,8 +4,8 @@
 // What bounds it: a decoding step reads each cached code and factor once
 // (1.125 hd bytes a slot and KV head) and does 4 hd operations per query head
 // on it.  One token over 131072 slots of 8 heads of 128: 151 MB, 23 us at the
-// copy rate; the kernel takes 40 us (3.8 TB/s), of which the loads alone take
-// 31 and the arithmetic alone 35: 650 instructions a tile of 32 slots and head,
+// copy rate; the kernel takes 40 us (3.8 TB/s; 43 with the one that joins its
+// parts), of which the loads alone take 31 and the arithmetic alone 35: 650 instructions a tile of 32 slots and head,
 // 256 of them the codes' conversion (a cvt and a multiply per two elements),
 // 34 products; the integer pipe is at 49 %, issue slots at 55 %, no pipe full.
 // Short calls are bound by the chain of dependent loads, about 3 us.

@@ -15,11 +15,11 @@
 // Two CTAs share an SM (hd <= 192), so that one's products run beside the
 // other's conversions and exponentials.  Inside a CTA only the warp that issues P V
 // waits for all of P and V; the others go on to the next tile's K.
-// Measured, 512 tokens of 16/8 heads of 128 over 4608 positions: 46.3 us, 394
-// TFLOP/s (the warps' products took 142 us; with block-wide barriers in those
-// places and one exponential's argument to an instruction 47.9); a tile takes
-// 3600 clocks of an SM against the 1024 of its bound, in the latency of its
-// dependent steps; a call costs 10 us before and behind its tiles.
+// Measured, 512 tokens of 16/8 heads of 128 over 4608 positions: 47 us, 390
+// TFLOP/s (46.6 to 47.1 in repeats; the warps' products took 142; with block-wide
+// barriers in those places and one exponential's argument to an instruction
+// 47.9); a tile takes 3600 clocks of an SM against the 1024 of its bound, in the
+// latency of its dependent steps; a call costs 10 us before and behind its tiles.
 //
 // Operand layouts: Q and K as rows of 64 dimensions (128 bytes) with the
 // 128-byte swizzle, k-major; V in the same form, which read as the B operand of

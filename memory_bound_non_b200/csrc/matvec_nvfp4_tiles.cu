@@ -18,7 +18,8 @@
 // 16384 18 us (3.1 us of bytes, 1.7 of products), 62 of 256 to 11682 5.0 us; a
 // step takes 1600 clocks, a chain of conversion, barrier and sums in which no
 // single part stands out (without x 16 % less, without the factors' sums 14 %,
-// without the products 2 %).
+// without the products 2 %).  At 65 to 128 rows with such factors the sums in
+// registers spill (240 bytes a thread for bf16 rows, 372 for block-scaled FP8).
 #include <algorithm>
 
 #include "matvec_nvfp4.cuh"

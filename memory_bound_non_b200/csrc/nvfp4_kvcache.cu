@@ -16,7 +16,7 @@
 // their bytes at the copy rate: half the issue slots (K's exact products and the
 // 16-bit unpacking) and the wait for rows at random positions of the tables.
 // With one head to a lane group and 64-bit index arithmetic it took 39 us.  A
-// few tokens are bound by the launch (4.2 us with the reader, two launches).
+// few tokens are bound by the launch (ten: 5.6 us with the reader, two launches).
 //
 // K decides its codes next to e2m1 borders, so y has to be the exact value
 // rounded once: products as exact pairs (p, e) by FMA, their difference by
